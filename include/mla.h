@@ -379,6 +379,70 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
                                  const void* ctx, const void* k_nope, const void* v, int T,
                                  int L, void* o, float* lse, void* stream);
 
+/* Norms, rotation and append in one pass.  The pages describe MLA without
+ * norms; models of this shape norm what is projected before it is rotated and
+ * cached.  For each t < T, with y[t] = [q_1 .. q_H | c | k_rope] as
+ * mla_project writes it for W_A0 (row stride y_stride_tok) and
+ *   n(x, w) = x / sqrt(mean(x^2) + eps) * w     (x itself where w is NULL):
+ *   [u_i ; r_i] = n(q_i, w_q)          over all d_nope + d_rope numbers
+ *   q[t][i][0 : d_nope] = u_i;  RoPE(r_i, pos[t]) goes to
+ *   qbuf[t][i][d_latent : ], or to q[t][i][d_nope : ] where qbuf is NULL
+ *   row = [n(c, w_c) ; RoPE(n(k_rope, w_kr), pos[t])]  goes to the cache slot
+ *   (batch_idx[t], slot[t]) where pool is not NULL, and to ckr[t] where ckr is
+ *   not NULL.
+ * The key's norms act on what is cached: a per-head norm of W_UK c would not
+ * commute with the absorption.  pos is the token's position (the angle), slot
+ * its place in the sequence's pages; they differ once tokens were evicted.
+ * fp32 throughout, angles in fp64, one rounding to the dtype at the end.
+ * w_q: device [d_nope + d_rope], w_c: [d_latent], w_kr: [d_rope], dtype of
+ * dims, each may be NULL; eps > 0.  q: device, token t head i at
+ * t*q_stride_tok + i*(d_nope+d_rope); qbuf: device [T, H, d_latent + d_rope];
+ * ckr: device rows of d_latent + d_rope at stride ckr_stride_tok (what
+ * mla_cache_append_fp8 takes).  q may be y, and ckr the end of y's rows
+ * (y + H*(d_nope+d_rope)), with y's stride; no other overlap.  page_table:
+ * device int32 [n_seqs, max_pages].  A sequence, slot or page outside them or
+ * the pool skips that append and raises MLA_ERR_BOUNDS.  Both
+ * dtypes, any widths; DeepSeek-V2's, 16-byte aligned, take the fast kernel. */
+mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, const void* w_q,
+                         const void* w_c, const void* w_kr, float eps, const int32_t* pos,
+                         const int32_t* batch_idx, const int32_t* slot,
+                         const int32_t* page_table, int n_seqs, int max_pages, void* pool,
+                         int n_pages, void* q, int q_stride_tok, void* qbuf, void* ckr,
+                         int ckr_stride_tok, int T, void* stream);
+
+/* Eviction from the cache by gathered attention weight.  For each sequence b
+ * with L = seq_lens[b] cached tokens in slots 0 .. L-1:
+ *   a slot is free when its token's position (slot_pos[b*stride + slot], or
+ *   the slot itself where slot_pos is NULL) is >= n_sink and < end - n_recent,
+ *   end = 1 + the largest position among the L slots;
+ *   the n_out = min(max(L - budget[b], 0), free slots) free slots with the
+ *   smallest weights[b*stride + slot] leave, the lower slot first among
+ *   equals (-0 equals 0; NaN counts as more than +inf);
+ *   new_lens[b] = L - n_out, and the k-th remaining slot >= new_lens[b] moves
+ *   into the k-th vacated slot < new_lens[b]: cache row, weight, position.
+ * The slots 0 .. new_lens[b]-1 then hold the survivors; attention does not
+ * depend on their order, since a RoPE key carries its position.  Slots from
+ * new_lens[b] on keep their contents; whole pages among them may be reused.
+ * pool: device [n_pages, page_size] rows of dims' type, or of
+ * MLA_FP8_ROW_BYTES bytes where fp8_rows is not 0 (8-bit cache; else
+ * MLA_ERR_UNSUPPORTED).  Rows move in place: no page may belong to two
+ * sequences.  weights, new_weights: device fp32 [B, stride]; slot_pos,
+ * new_pos: device int32 [B, stride], each may be NULL (new_pos NULL: positions
+ * are not kept); entries < new_lens[b] of new_weights and new_pos are written.
+ * new_weights may be weights, new_pos slot_pos, new_lens seq_lens.  budget:
+ * device int32 [B], < 0 counts as 0.  stride >= every length.  B <= 65535.
+ * workspace: device, >= mla_cache_evict_workspace_size bytes, 256-byte
+ * aligned, contents ignored.  A length outside [0, min(stride,
+ * max_pages*page_size)] leaves that sequence as it was and raises
+ * MLA_ERR_BOUNDS; so does a page id outside the pool, for the rows it holds. */
+size_t mla_cache_evict_workspace_size(const mla_dims* dims, int B, int stride);
+mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp8_rows,
+                           const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                           int B, const float* weights, const int32_t* slot_pos, int stride,
+                           const int32_t* budget, int n_sink, int n_recent, float* new_weights,
+                           int32_t* new_pos, int32_t* new_lens, void* workspace,
+                           size_t ws_bytes, void* stream);
+
 /* Synchronises `stream`, then returns and clears the device status word of
  * the current device (MLA_OK, MLA_ERR_TIMEOUT or MLA_ERR_BOUNDS; TIMEOUT
  * wins if both were raised), or MLA_ERR_CUDA if the stream failed. */

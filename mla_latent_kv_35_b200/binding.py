@@ -29,7 +29,8 @@ EXPORTS = ("mla_project", "mla_absorb_q", "mla_rope", "mla_cache_append",
            "mla_decode_noalloc", "mla_pre_attention", "mla_decode_partial",
            "mla_combine_parts", "mla_decode_config", "mla_decode_noalloc_scratch_bytes",
            "mla_cache_append_fp8", "mla_cache_quantize_fp8", "mla_decode_fp8",
-           "mla_decode_fp8_workspace_size", "mla_prefill_rebuild_kv", "mla_prefill_attention")
+           "mla_decode_fp8_workspace_size", "mla_prefill_rebuild_kv", "mla_prefill_attention",
+           "mla_norm_rope", "mla_cache_evict_workspace_size", "mla_cache_evict")
 
 
 class MLAError(RuntimeError):
@@ -112,6 +113,11 @@ _SIGS = {
                         _P, _P, _P], _I),
     "mla_prefill_rebuild_kv": ([ctypes.POINTER(Dims), _P, _I, _P, _I, _P, _P, _P, _P, _P, _P],
                                _I),
+    "mla_norm_rope": ([ctypes.POINTER(Dims), _P, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
+                       _I, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P], _I),
+    "mla_cache_evict_workspace_size": ([ctypes.POINTER(Dims), _I, _I], _Z),
+    "mla_cache_evict": ([ctypes.POINTER(Dims), _P, _I, _I, _P, _I, _P, _I, _P, _P, _I, _P, _I, _I,
+                         _P, _P, _P, _P, _Z, _P], _I),
     "mla_prefill_attention": ([ctypes.POINTER(Dims), _P, _I, _P, _P, _P, _I, _I, _P, _P, _P], _I),
 }
 
@@ -153,6 +159,40 @@ def _dev(*ts):
     for t in ts:
         if t is not None and not t.is_cuda:
             raise ValueError("tensors must live on the CUDA device")
+
+
+def _ref(dims: MLADims):
+    """The dims struct by reference, built once per MLADims."""
+    c = dims.__dict__.get("_ref")
+    if c is None:
+        c = ctypes.byref(dims.c())
+        object.__setattr__(dims, "_ref", c)
+    return c
+
+
+def _here(dev: int, what: str, t, dtype, numel: int) -> int:
+    """Address of a tensor that must be on the current device `dev`, contiguous, of `dtype` and
+    at least `numel` elements."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: the tensor must live on the current CUDA device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    if t.numel() < numel or not t.is_contiguous():
+        raise ValueError(f"{what}: expected a contiguous tensor of at least {numel} elements")
+    return t.data_ptr()
+
+
+def _rows(dev: int, what: str, t, dtype, rows: int, width: int, stride: int) -> int:
+    """Address of `rows` rows of `width` elements, `stride` apart, on the current device; the
+    tensor is a view of them whose storage holds them all."""
+    if t.get_device() != dev:
+        raise ValueError(f"{what}: the tensor must live on the current CUDA device")
+    if t.dtype is not dtype:
+        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
+    need = (t.storage_offset() + (rows - 1) * stride + width) * t.element_size() if rows > 0 else 0
+    if stride < width or t.untyped_storage().nbytes() < need:
+        raise ValueError(f"{what}: the tensor does not hold {rows} rows of {width} at stride {stride}")
+    return t.data_ptr()
 
 
 # --------------------------------------------------------------------------
@@ -303,6 +343,61 @@ def mla_out_proj(dims: MLADims, o_lat, w_uv, w_o, scratch, out, T: int):
     _check("mla_out_proj", lib().mla_out_proj(ctypes.byref(dims.c()), _ptr(o_lat), _ptr(w_uv),
                                               _ptr(w_o), _ptr(scratch), sb, _ptr(out), T,
                                               _stream()))
+
+
+def mla_norm_rope(dims: MLADims, y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batch_idx, slot,
+                  page_table, max_pages, pool, n_pages, q, q_stride_tok, qbuf, ckr,
+                  ckr_stride_tok, T):
+    """RMS norms of the query heads, the latent and the RoPE key (weights w_q, w_c, w_kr, each or
+    None), the rotation by pos and the append at slot, in one pass over the A0 rows y.  pool,
+    qbuf and ckr may be None (include/mla.h)."""
+    dev = torch.cuda.current_device()
+    dt, i32 = dims.torch_dtype, torch.int32
+    H, dqk = dims.n_heads, dims.d_nope + dims.d_rope
+    D = dims.d_latent + dims.d_rope
+    _check("mla_norm_rope", lib().mla_norm_rope(
+        _ref(dims), _rows(dev, "y", y, dt, T, H * dqk + D, y_stride_tok), y_stride_tok,
+        None if w_q is None else _here(dev, "w_q", w_q, dt, dqk),
+        None if w_c is None else _here(dev, "w_c", w_c, dt, dims.d_latent),
+        None if w_kr is None else _here(dev, "w_kr", w_kr, dt, dims.d_rope), eps,
+        _here(dev, "pos", pos, i32, T),
+        None if pool is None else _here(dev, "batch_idx", batch_idx, i32, T),
+        None if pool is None else _here(dev, "slot", slot, i32, T),
+        None if pool is None else _here(dev, "page_table", page_table, i32, max_pages),
+        0 if pool is None else page_table.numel() // max_pages, max_pages,
+        None if pool is None else _here(dev, "pool", pool, dt, n_pages * dims.page_size * D),
+        n_pages, _rows(dev, "q", q, dt, T, H * dqk, q_stride_tok), q_stride_tok,
+        None if qbuf is None else _here(dev, "qbuf", qbuf, dt, T * H * D),
+        None if ckr is None else _rows(dev, "ckr", ckr, dt, T, D, ckr_stride_tok), ckr_stride_tok,
+        T, torch._C._cuda_getCurrentRawStream(dev)))
+
+
+def mla_cache_evict_workspace_size(dims: MLADims, B: int, stride: int) -> int:
+    return int(lib().mla_cache_evict_workspace_size(_ref(dims), B, stride))
+
+
+def mla_cache_evict(dims: MLADims, pool, n_pages, fp8_rows, page_table, max_pages, seq_lens, B,
+                    weights, slot_pos, stride, budget, n_sink, n_recent, new_weights, new_pos,
+                    new_lens, workspace):
+    """Cut every sequence to its budget: the cached tokens with the least gathered weight leave,
+    the first n_sink and the last n_recent positions excepted, and the survivors behind the new
+    end move into the vacated slots (include/mla.h).  fp8_rows: pool is the 8-bit cache."""
+    dev = torch.cuda.current_device()
+    i32, f32 = torch.int32, torch.float32
+    row = FP8_ROW_BYTES if fp8_rows else dims.d_latent + dims.d_rope
+    _check("mla_cache_evict", lib().mla_cache_evict(
+        _ref(dims), _here(dev, "pool", pool, torch.uint8 if fp8_rows else dims.torch_dtype,
+                          n_pages * dims.page_size * row), n_pages, 1 if fp8_rows else 0,
+        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+        _here(dev, "seq_lens", seq_lens, i32, B), B,
+        _here(dev, "weights", weights, f32, B * stride),
+        None if slot_pos is None else _here(dev, "slot_pos", slot_pos, i32, B * stride), stride,
+        _here(dev, "budget", budget, i32, B), n_sink, n_recent,
+        _here(dev, "new_weights", new_weights, f32, B * stride),
+        None if new_pos is None else _here(dev, "new_pos", new_pos, i32, B * stride),
+        _here(dev, "new_lens", new_lens, i32, B),
+        _here(dev, "workspace", workspace, torch.uint8, 0), workspace.numel(),
+        torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def mla_get_device_status() -> int:

@@ -14,8 +14,10 @@
 #include "common.cuh"
 #include "decode_fp8.cuh"
 #include "decode_tc.cuh"
+#include "evict.cuh"
 #include "fp8.cuh"
 #include "gemm_tc.cuh"
+#include "norm_rope.cuh"
 #include "prefill_tc.cuh"
 #include "simt.cuh"
 
@@ -814,6 +816,139 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
                                                 as_stream(stream));
   g_launches.fetch_add(1, std::memory_order_relaxed);
   return s;
+}
+
+// ---------------------------------------------------------------------------
+// norms, rotation and append in one pass
+// ---------------------------------------------------------------------------
+mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, const void* w_q,
+                         const void* w_c, const void* w_kr, float eps, const int32_t* pos,
+                         const int32_t* batch_idx, const int32_t* slot, const int32_t* page_table,
+                         int n_seqs, int max_pages, void* pool, int n_pages, void* q,
+                         int q_stride_tok, void* qbuf, void* ckr, int ckr_stride_tok, int T, void* stream) {
+  if (!dims_ok(dims) || T < 0 || !(eps > 0.f) || !std::isfinite(eps)) return MLA_ERR_INVALID_ARG;
+  const int H = dims->n_heads, dn = dims->d_nope, dc = dims->d_latent, dr = dims->d_rope;
+  const long long dqk = dn + dr, D = dc + dr;
+  if ((long long)y_stride_tok < H * dqk + D || (long long)q_stride_tok < H * dqk ||
+      (ckr != nullptr && (long long)ckr_stride_tok < D) ||
+      (pool != nullptr && (n_seqs < 1 || max_pages < 1 || n_pages < 1)))
+    return MLA_ERR_INVALID_ARG;
+  if (T == 0) return MLA_OK;
+  if (!y || !q || !pos || (pool != nullptr && (!batch_idx || !slot || !page_table)))
+    return MLA_ERR_INVALID_ARG;
+  NormRopeArgs a{};
+  a.y = y; a.ys_tok = y_stride_tok;
+  a.w_q = w_q; a.w_c = w_c; a.w_kr = w_kr;
+  a.pos = pos; a.batch_idx = batch_idx; a.slot = slot; a.page_table = page_table;
+  a.pool = pool;
+  a.q = q; a.qs_tok = q_stride_tok;
+  a.qbuf = qbuf;
+  a.ckr = ckr; a.cs_tok = ckr_stride_tok;
+  a.H = H; a.d_nope = dn; a.d_rope = dr; a.d_latent = dc;
+  a.n_seqs = n_seqs; a.max_pages = max_pages; a.n_pages = n_pages;
+  a.page_size = dims->page_size; a.T = T;
+  a.eps = eps;
+  a.base = (double)dims->rope_base;
+  cudaStream_t st = as_stream(stream);
+  const int E = dims->dtype == MLA_F32 ? 4 : 8;   // numbers per 16 bytes
+  const bool wide = dn == kNormDN && dr == kNormDR && dc == kNormDC && y_stride_tok % E == 0 &&
+                    q_stride_tok % E == 0 && (ckr == nullptr || ckr_stride_tok % E == 0) &&
+                    aligned16(y) && aligned16(w_q) && aligned16(w_c) && aligned16(w_kr) &&
+                    aligned16(pool) && aligned16(q) && aligned16(qbuf) && aligned16(ckr);
+  if (wide) {
+    // base^(-2k/64) as powers of base^(-1/32): 31 products are within 2^-47
+    // of it, 10^-9 rad at position 131072
+    const double step = std::pow(a.base, -2.0 / kNormDR);
+    a.freq[0] = 1.0;
+    for (int k = 1; k < kNormDR / 2; ++k) a.freq[k] = a.freq[k - 1] * step;
+    const long long blocks = (long long)T * ((H + kNormHeads - 1) / kNormHeads) +
+                             (T + kNormThreads / 32 - 1) / (kNormThreads / 32);
+    if (blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+    if (dims->dtype == MLA_F32)
+      norm_rope_kernel<float><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+    else
+      norm_rope_kernel<__nv_bfloat16><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+    return check_launch();
+  }
+  const long long blocks = ((long long)T * (H + 2) + kNormThreads / 32 - 1) / (kNormThreads / 32);
+  if (blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
+  if (dims->dtype == MLA_F32)
+    norm_rope_any_kernel<float><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+  else
+    norm_rope_any_kernel<__nv_bfloat16><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+  return check_launch();
+}
+
+// ---------------------------------------------------------------------------
+// eviction by gathered attention weight
+// ---------------------------------------------------------------------------
+// Workspace: the pairs [B][stride], then their counts [B].
+size_t mla_cache_evict_workspace_size(const mla_dims* dims, int B, int stride) {
+  if (!dims_ok(dims) || B < 0 || stride < 1) return 0;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  return up((size_t)B * stride * sizeof(int2)) + up((size_t)B * sizeof(int32_t));
+}
+
+mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp8_rows,
+                           const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                           int B, const float* weights, const int32_t* slot_pos, int stride,
+                           const int32_t* budget, int n_sink, int n_recent, float* new_weights,
+                           int32_t* new_pos, int32_t* new_lens, void* workspace, size_t ws_bytes,
+                           void* stream) {
+  if (!dims_ok(dims) || B < 0 || B > 65535 || stride < 1 || n_pages < 1 || max_pages < 1 ||
+      n_sink < 0 || n_recent < 0)
+    return MLA_ERR_INVALID_ARG;
+  if ((long long)max_pages * dims->page_size > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
+  if (fp8_rows && !fp8_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
+  if (B == 0) return MLA_OK;
+  if (!pool || !page_table || !seq_lens || !weights || !budget || !new_weights || !new_lens ||
+      !workspace)
+    return MLA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      ws_bytes < mla_cache_evict_workspace_size(dims, B, stride))
+    return MLA_ERR_INVALID_ARG;
+  cudaStream_t st = as_stream(stream);
+  EvictArgs a{};
+  a.seq_lens = seq_lens; a.budget = budget; a.weights = weights; a.slot_pos = slot_pos;
+  a.new_weights = new_weights; a.new_pos = new_pos; a.new_lens = new_lens;
+  a.pairs = static_cast<int2*>(workspace);
+  a.n_pairs = reinterpret_cast<int32_t*>(
+      static_cast<char*>(workspace) +
+      (((size_t)B * stride * sizeof(int2) + 255) & ~(size_t)255));
+  a.stride = stride;
+  a.max_tokens = max_pages * dims->page_size;
+  a.n_sink = n_sink; a.n_recent = n_recent;
+  int cluster = 1;
+  while (cluster < kEvictMaxCluster && stride > (long long)kEvictSlotsPerBlock * cluster)
+    cluster *= 2;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3((unsigned)(B * cluster));
+  cfg.blockDim = dim3(kEvictThreads);
+  cfg.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = (unsigned)cluster;
+  at[0].val.clusterDim.y = 1;
+  at[0].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, evict_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  MLA_TRY(check_launch());
+  const long long row_bytes = fp8_rows ? fp8::kRowBytes
+                                       : (long long)(dims->d_latent + dims->d_rope) *
+                                             (dims->dtype == MLA_F32 ? 4 : 2);
+  // about eight blocks per SM over all sequences
+  const long long x = (8LL * sm_count() + B - 1) / B;
+  dim3 grid((unsigned)std::min<long long>(x, ((long long)stride + 7) / 8), (unsigned)B);
+  if (row_bytes % 16 == 0 && aligned16(pool))
+    evict_move_kernel<uint4><<<grid, 256, 0, st>>>(
+        static_cast<uint4*>(pool), (int)(row_bytes / 16), n_pages, dims->page_size, page_table,
+        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, stride);
+  else
+    evict_move_kernel<uint16_t><<<grid, 256, 0, st>>>(
+        static_cast<uint16_t*>(pool), (int)(row_bytes / 2), n_pages, dims->page_size, page_table,
+        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, stride);
+  return check_launch();
 }
 
 }  // extern "C"

@@ -25,3 +25,9 @@ from .mla_oracle import (  # noqa: F401
     quantize_latent_fp8,
     dequantize_fp8,
 )
+from .serving_oracle import (  # noqa: F401
+    rms_norm,
+    norm_rope,
+    attention_weights,
+    evict,
+)
