@@ -379,6 +379,46 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
                                  const void* ctx, const void* k_nope, const void* v, int T,
                                  int L, void* o, float* lse, void* stream);
 
+/* A4 + A5 for chunks of any length ([DF-0], [DF-1]; the pages give the
+ * attention, the batching of chunks is an addition of this library).  Sequence
+ * b brings the query tokens cu_q[b] .. cu_q[b+1]-1, T_b of them, which are the
+ * last T_b of its L = seq_lens[b] cached tokens.  For query j < T_b of
+ * sequence b, token u = cu_q[b] + j, and head i:
+ *   s_t = scale * qbuf[u, i, :] . pool_row(b, t),  p = softmax over
+ *   t <= L - T_b + j,   o_lat[u, i, :] = sum_t p_t pool_row(b, t)[0 : d_latent]
+ *   lse[u, i] = ln sum_t exp(s_t)
+ * qbuf: device bf16 [total_q, H, d_latent + d_rope]; cu_q: device int32
+ * [B + 1], ascending from 0 to at most total_q, no chunk longer than max_q
+ * (T_b = 0 is allowed); pool, page_table, seq_lens as for mla_decode; o_lat:
+ * device bf16 [total_q, H, d_latent] (the input of mla_out_proj_bf16); lse:
+ * device fp32 [total_q, H].  Rows from cu_q[B] on are left as they were.
+ * Accumulation, softmax and merges are fp32; p is rounded to bf16 for the
+ * value product and o_lat when it is stored.  workspace: device, >=
+ * mla_chunk_attention_workspace_size bytes, 256-byte aligned, contents
+ * ignored.  qbuf, pool and o_lat 16-byte aligned.  Needs dtype MLA_BF16,
+ * d_latent == 512, d_rope == 64, page_size == 64 (else MLA_ERR_UNSUPPORTED,
+ * workspace size 0), any n_heads, total_q * H + 128 * B < 2^31.  A cu_q that
+ * breaks its rules anywhere leaves every row as it was; a chunk with L < T_b
+ * or L > max_pages*page_size gets o_lat = 0, lse = -inf; both raise
+ * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as
+ * rows of zeros.  Many queries of one sequence are cheaper in the non-absorbed
+ * form (mla_prefill_attention), from a few hundred on. */
+size_t mla_chunk_attention_workspace_size(const mla_dims* dims, int B, int total_q, int max_q);
+mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int32_t* cu_q,
+                               int total_q, int max_q, const void* pool, int n_pages,
+                               const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                               int B, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
+                               void* stream);
+
+/* A6 on bf16 rows, as mla_chunk_attention writes them: mla_out_proj without
+ * the conversion.  o_lat: device bf16 [T, H, d_latent], 16-byte aligned;
+ * scratch: >= mla_out_proj_bf16_scratch_size bytes.  bf16 only (else
+ * MLA_ERR_UNSUPPORTED). */
+size_t mla_out_proj_bf16_scratch_size(const mla_dims* dims, int T);
+mla_status mla_out_proj_bf16(const mla_dims* dims, const void* o_lat, const void* w_uv,
+                             const void* w_o, void* scratch, size_t scratch_bytes, float* out,
+                             int T, void* stream);
+
 /* Norms, rotation and append in one pass.  The pages describe MLA without
  * norms; models of this shape norm what is projected before it is rotated and
  * cached.  For each t < T, with y[t] = [q_1 .. q_H | c | k_rope] as

@@ -30,6 +30,8 @@ EXPORTS = ("mla_project", "mla_absorb_q", "mla_rope", "mla_cache_append",
            "mla_combine_parts", "mla_decode_config", "mla_decode_noalloc_scratch_bytes",
            "mla_cache_append_fp8", "mla_cache_quantize_fp8", "mla_decode_fp8",
            "mla_decode_fp8_workspace_size", "mla_prefill_rebuild_kv", "mla_prefill_attention",
+           "mla_chunk_attention_workspace_size", "mla_chunk_attention",
+           "mla_out_proj_bf16_scratch_size", "mla_out_proj_bf16",
            "mla_norm_rope", "mla_cache_evict_workspace_size", "mla_cache_evict")
 
 
@@ -113,6 +115,11 @@ _SIGS = {
                         _P, _P, _P], _I),
     "mla_prefill_rebuild_kv": ([ctypes.POINTER(Dims), _P, _I, _P, _I, _P, _P, _P, _P, _P, _P],
                                _I),
+    "mla_chunk_attention_workspace_size": ([ctypes.POINTER(Dims), _I, _I, _I], _Z),
+    "mla_chunk_attention": ([ctypes.POINTER(Dims), _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _Z,
+                             _P, _P, _P], _I),
+    "mla_out_proj_bf16_scratch_size": ([ctypes.POINTER(Dims), _I], _Z),
+    "mla_out_proj_bf16": ([ctypes.POINTER(Dims), _P, _P, _P, _P, _Z, _P, _I, _P], _I),
     "mla_norm_rope": ([ctypes.POINTER(Dims), _P, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
                        _I, _I, _P, _I, _P, _I, _P, _P, _I, _I, _P], _I),
     "mla_cache_evict_workspace_size": ([ctypes.POINTER(Dims), _I, _I], _Z),
@@ -343,6 +350,47 @@ def mla_out_proj(dims: MLADims, o_lat, w_uv, w_o, scratch, out, T: int):
     _check("mla_out_proj", lib().mla_out_proj(ctypes.byref(dims.c()), _ptr(o_lat), _ptr(w_uv),
                                               _ptr(w_o), _ptr(scratch), sb, _ptr(out), T,
                                               _stream()))
+
+
+def mla_chunk_attention_workspace_size(dims: MLADims, B: int, total_q: int, max_q: int) -> int:
+    return int(lib().mla_chunk_attention_workspace_size(_ref(dims), B, total_q, max_q))
+
+
+def mla_chunk_attention(dims: MLADims, qbuf, cu_q, total_q, max_q, pool, n_pages, page_table,
+                        max_pages, seq_lens, B, workspace, o_lat, lse):
+    """Attention of ragged chunks of new tokens over the paged cache: sequence b's queries are
+    tokens cu_q[b] .. cu_q[b + 1] - 1 of qbuf and the last of its seq_lens[b] cached tokens
+    (include/mla.h).  o_lat bf16, lse fp32."""
+    dev = torch.cuda.current_device()
+    dt, i32 = dims.torch_dtype, torch.int32
+    H, D = dims.n_heads, dims.d_latent + dims.d_rope
+    _check("mla_chunk_attention", lib().mla_chunk_attention(
+        _ref(dims), _here(dev, "qbuf", qbuf, dt, total_q * H * D),
+        _here(dev, "cu_q", cu_q, i32, B + 1), total_q, max_q,
+        _here(dev, "pool", pool, dt, n_pages * dims.page_size * D), n_pages,
+        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+        _here(dev, "seq_lens", seq_lens, i32, B), B,
+        _here(dev, "workspace", workspace, torch.uint8, 0), workspace.numel(),
+        _here(dev, "o_lat", o_lat, dt, total_q * H * dims.d_latent),
+        _here(dev, "lse", lse, torch.float32, total_q * H),
+        torch._C._cuda_getCurrentRawStream(dev)))
+
+
+def mla_out_proj_bf16_scratch_size(dims: MLADims, T: int) -> int:
+    return int(lib().mla_out_proj_bf16_scratch_size(_ref(dims), T))
+
+
+def mla_out_proj_bf16(dims: MLADims, o_lat, w_uv, w_o, scratch, out, T: int):
+    """mla_out_proj of bf16 rows (mla_chunk_attention's output)."""
+    dev = torch.cuda.current_device()
+    dt, H, hv = dims.torch_dtype, dims.n_heads, dims.n_heads * dims.d_v
+    _check("mla_out_proj_bf16", lib().mla_out_proj_bf16(
+        _ref(dims), _here(dev, "o_lat", o_lat, dt, T * H * dims.d_latent),
+        _here(dev, "w_uv", w_uv, dt, hv * dims.d_latent),
+        _here(dev, "w_o", w_o, dt, dims.d_model * hv),
+        _here(dev, "scratch", scratch, torch.uint8, 0), scratch.numel(),
+        _here(dev, "out", out, torch.float32, T * dims.d_model), T,
+        torch._C._cuda_getCurrentRawStream(dev)))
 
 
 def mla_norm_rope(dims: MLADims, y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batch_idx, slot,

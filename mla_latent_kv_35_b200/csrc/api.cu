@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "../../include/mla.h"
+#include "chunk_tc.cuh"
 #include "common.cuh"
 #include "decode_fp8.cuh"
 #include "decode_tc.cuh"
@@ -721,6 +722,10 @@ size_t mla_out_proj_scratch_size(const mla_dims* dims, int T) {
          up((size_t)w_o_splits(dims, T) * T * dims->d_model * 4);
 }
 
+static mla_status out_proj_bf16(const mla_dims* dims, const __nv_bfloat16* olb, const void* w_uv,
+                                const void* w_o, char* scratch, float* out, int T,
+                                cudaStream_t st);
+
 mla_status mla_out_proj(const mla_dims* dims, const float* o_lat, const void* w_uv,
                         const void* w_o, void* scratch, size_t scratch_bytes, float* out, int T,
                         void* stream) {
@@ -744,11 +749,41 @@ mla_status mla_out_proj(const mla_dims* dims, const float* o_lat, const void* w_
   }
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   __nv_bfloat16* olb = static_cast<__nv_bfloat16*>(scratch);
-  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(static_cast<char*>(scratch) +
-                                                      up((size_t)T * H * dc * 2));
   const long long n = (long long)T * H * dc;
   cast_f32_bf16_kernel<<<(unsigned)((n / 4 + 255) / 256 + 1), 256, 0, st>>>(o_lat, olb, n);
   MLA_TRY(check_launch());
+  return out_proj_bf16(dims, olb, w_uv, w_o,
+                       static_cast<char*>(scratch) + up((size_t)T * H * dc * 2), out, T, st);
+}
+
+size_t mla_out_proj_bf16_scratch_size(const mla_dims* dims, int T) {
+  if (!dims_ok(dims) || T < 0 || dims->dtype != MLA_BF16) return 0;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  return up((size_t)T * dims->n_heads * dims->d_v * 2) +
+         up((size_t)w_o_splits(dims, T) * T * dims->d_model * 4);
+}
+
+mla_status mla_out_proj_bf16(const mla_dims* dims, const void* o_lat, const void* w_uv,
+                             const void* w_o, void* scratch, size_t scratch_bytes, float* out,
+                             int T, void* stream) {
+  if (!dims_ok(dims) || T < 0) return MLA_ERR_INVALID_ARG;
+  if (dims->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
+  if (T == 0) return MLA_OK;
+  if (!o_lat || !w_uv || !w_o || !scratch || !out) return MLA_ERR_INVALID_ARG;
+  if (scratch_bytes < mla_out_proj_bf16_scratch_size(dims, T) ||
+      (reinterpret_cast<uintptr_t>(scratch) & 255u) != 0)
+    return MLA_ERR_INVALID_ARG;
+  return out_proj_bf16(dims, static_cast<const __nv_bfloat16*>(o_lat), w_uv, w_o,
+                       static_cast<char*>(scratch), out, T, as_stream(stream));
+}
+
+// The bf16 products of A6: W_UV per head into the scratch, then W_O.
+static mla_status out_proj_bf16(const mla_dims* dims, const __nv_bfloat16* olb, const void* w_uv,
+                                const void* w_o, char* scratch, float* out, int T,
+                                cudaStream_t st) {
+  const int H = dims->n_heads, dc = dims->d_latent, dv = dims->d_v, dm = dims->d_model;
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  __nv_bfloat16* o = reinterpret_cast<__nv_bfloat16*>(scratch);
   // o[t, i, :] = W_UV[i] o_lat[t, i, :]
   MLA_TRY(launch_tc_gemm(w_uv, false, (long long)dv * dc, olb, (long long)H * dc, dc, dv, T, dc, H,
                          o, dv, (long long)H * dv, 1, kOutBf16, st));
@@ -815,6 +850,51 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
                                                 static_cast<__nv_bfloat16*>(o), lse,
                                                 as_stream(stream));
   g_launches.fetch_add(1, std::memory_order_relaxed);
+  return s;
+}
+
+// ---------------------------------------------------------------------------
+// ragged chunks over the paged cache
+// ---------------------------------------------------------------------------
+// DeepSeek-V2's cache rows in 64-token pages, bf16.
+static bool chunk_dims_ok(const mla_dims* d) {
+  return d->dtype == MLA_BF16 && d->d_latent == dtc::kDC && d->d_rope == dtc::kD - dtc::kDC &&
+         d->page_size == dtc::kPage;
+}
+
+// Query rows and virtual sequences are counted in 32 bits.
+static bool chunk_sizes_ok(const mla_dims* d, int B, int total_q, int max_q) {
+  return B >= 0 && total_q >= 0 && max_q >= 0 && max_q <= total_q &&
+         (long long)total_q * d->n_heads + 128LL * B < 0x7FFFFFFFll;
+}
+
+size_t mla_chunk_attention_workspace_size(const mla_dims* dims, int B, int total_q, int max_q) {
+  if (!dims_ok(dims) || !chunk_dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q)) return 0;
+  return chunk_layout(total_q, B, dims->n_heads, sm_count() / 2).total;
+}
+
+mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int32_t* cu_q,
+                               int total_q, int max_q, const void* pool, int n_pages,
+                               const int32_t* page_table, int max_pages, const int32_t* seq_lens,
+                               int B, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
+                               void* stream) {
+  if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 || max_pages < 1 ||
+      (long long)max_pages * dims->page_size > 0x7FFFFFFFll)
+    return MLA_ERR_INVALID_ARG;
+  if (!chunk_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
+  if (B == 0 || total_q == 0) return MLA_OK;
+  if (!qbuf || !cu_q || !pool || !page_table || !seq_lens || !workspace || !o_lat || !lse)
+    return MLA_ERR_INVALID_ARG;
+  if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 || !aligned16(qbuf) ||
+      !aligned16(pool) || !aligned16(o_lat))
+    return MLA_ERR_INVALID_ARG;
+  const ChunkLayout c = chunk_layout(total_q, B, dims->n_heads, sm_count() / 2);
+  if (ws_bytes < c.total) return MLA_ERR_INVALID_ARG;
+  const mla_status s = launch_chunk_tc_impl(
+      make_tmap_bf16, qbuf, cu_q, total_q, max_q, pool, n_pages, page_table, max_pages, seq_lens,
+      B, dims->n_heads, dims->scale, static_cast<char*>(workspace), c,
+      static_cast<__nv_bfloat16*>(o_lat), lse, as_stream(stream));
+  g_launches.fetch_add(3, std::memory_order_relaxed);
   return s;
 }
 

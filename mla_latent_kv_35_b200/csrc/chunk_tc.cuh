@@ -1,0 +1,249 @@
+// chunk_tc.cuh -- attention of ragged chunks of new tokens over the paged
+// latent cache, with the absorbed query.
+//
+// What it computes: mla_decode's attention (scores over the 576 cached
+// numbers, values the first 512) for chunks of any length: sequence b brings
+// T_b query tokens, the last T_b of its L_b cached tokens, and query j sees
+// tokens t <= L_b - T_b + j.  One launch covers decode tokens, speculative
+// tokens and prompt tails of a mixed batch.  Against rebuilt per-head keys
+// (prefill_tc.cuh) a query-token-head costs 1088 instead of 320
+// multiply-adds, but nothing is rebuilt: 512 x 256 multiply-adds per
+// (token, head), repaid from about 170 queries per sequence on.
+//
+// The tensor-core kernel is the decode's (decode_tc.cuh: pair MMAs, 128 query
+// rows per cluster, 256-token blocks), over another list of virtual
+// sequences.  Each chunk's T_b H rows are cut into blocks of 128; a block
+// visits only the token blocks that its last row sees.  All blocks of all
+// chunks are laid end to end and split evenly over one worker per pair of
+// SMs, so a batch of one long chunk and many short ones keeps every SM busy.
+//   * A worker's pieces that cover their virtual sequence whole are final:
+//     the epilogue writes bf16 rows and the LSE.  Only a worker's first and
+//     last piece can be partial, so 2 slots per worker hold all partial
+//     results (fp32), whatever the batch, and the merge (chunk_combine_kernel)
+//     reads the few virtual sequences that a worker boundary cuts.
+//   * o is stored in bf16: it is the W_UV product's input, and P is bf16.
+//
+// Bound: the tensor pipe and the loads that feed it.  128 rows meet each
+// 576-number row of the cache, 242 operations per byte read through L2.
+#pragma once
+
+#include "decode_tc.cuh"
+
+namespace mla {
+
+// Virtual sequences a batch can have: full blocks of 128 rows, and a partial
+// one per sequence.
+inline long long chunk_max_v(long long total_q, int B, int H) { return total_q * H / 128 + B; }
+
+// Block-wide exclusive prefix sum of one value per thread (1024 threads).
+__device__ __forceinline__ int block_exclusive(int x, int* warp_sums, int* total) {
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  int inc = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, inc, o);
+    if (lane >= o) inc += y;
+  }
+  if (lane == 31) warp_sums[w] = inc;
+  __syncthreads();
+  const int mine = warp_sums[lane];
+  int all = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int y = __shfl_up_sync(0xffffffffu, all, o);
+    if (lane >= o) all += y;
+  }
+  *total = __shfl_sync(0xffffffffu, all, 31);
+  const int before = __shfl_sync(0xffffffffu, all - mine, w);
+  __syncthreads();
+  return before + inc - x;
+}
+
+// Whether cu_q breaks its rules at sequence b: ascending within [0, total_q],
+// no chunk longer than max_q.
+__device__ __forceinline__ bool chunk_bad(const int32_t* cu_q, int b, int total_q, int max_q) {
+  const int a = cu_q[b], z = cu_q[b + 1];
+  return a < 0 || z < a || z > total_q || z - a > max_q;
+}
+
+// Virtual sequences of the batch, sequence by sequence, and the prefix sums
+// of their token blocks.  A cu_q that breaks its rules anywhere gives no
+// blocks at all: chunks could overlap.  A sequence whose length is impossible
+// keeps its rows with nothing to see (one empty block), so that they come out
+// as 0 and -inf.  first: [B + 1], scratch.
+__global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
+                                                          const int32_t* seq_lens, int B, int H,
+                                                          int total_q, int max_q, int max_tokens,
+                                                          int V, int32_t* first, VSeq* vseq,
+                                                          int32_t* start) {
+  __shared__ int warp_sums[32];
+  bool wrong = false;
+  for (int b = threadIdx.x; b < B; b += 1024) wrong |= chunk_bad(cu_q, b, total_q, max_q);
+  if (__syncthreads_or(wrong)) {
+    for (int v = threadIdx.x; v <= V; v += 1024) start[v] = 0;
+    if (threadIdx.x == 0) raise_flag(kFlagBounds);
+    return;
+  }
+  int base = 0;
+  for (int b0 = 0; b0 < B; b0 += 1024) {
+    const int b = b0 + threadIdx.x;
+    const int T = b < B ? cu_q[b + 1] - cu_q[b] : 0;
+    int sum;
+    const int off = block_exclusive((int)(((long long)T * H + 127) / 128), warp_sums, &sum);
+    if (b < B) first[b] = base + off;
+    base += sum;
+  }
+  if (threadIdx.x == 0) first[B] = base;
+  __syncthreads();
+  const int live = base;    // <= V, as the chunks do not overlap
+  int blocks = 0;
+  for (int v0 = 0; v0 < V; v0 += 1024) {
+    const int v = v0 + threadIdx.x;
+    int nb = 0;
+    if (v < live) {
+      const int b = seq_of_block(first, B, v);
+      VSeq s;
+      s.b = b;
+      s.row0 = (v - first[b]) * 128;
+      s.q0 = cu_q[b];
+      s.T = cu_q[b + 1] - s.q0;
+      s.L = seq_lens[b];
+      if (s.L < s.T || s.L > max_tokens) {
+        if (s.row0 == 0) raise_flag(kFlagBounds);
+        s.L = 0;
+        nb = 1;
+      } else {
+        const int last = min(s.T - 1, (s.row0 + 127) / H);      // last query of the block
+        nb = (s.L - s.T + last + 1 + dtc::kBlk - 1) / dtc::kBlk;
+      }
+      vseq[v] = s;
+    }
+    int sum;
+    const int off = block_exclusive(nb, warp_sums, &sum);
+    if (v < V) start[v] = blocks + off;
+    blocks += sum;
+  }
+  if (threadIdx.x == 0) start[V] = blocks;
+}
+
+// Merges the virtual sequences that worker boundaries cut.  Block (k, y)
+// looks at the boundary between workers k and k + 1: if it is the first one
+// inside its virtual sequence, the block's eight warps merge rows 8y .. 8y +
+// 7 of it, a warp per row.
+__global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse, const float* ws_o,
+                                                            const int32_t* start, const VSeq* vseq,
+                                                            int V, int H, int G, __nv_bfloat16* o,
+                                                            float* lse) {
+  const int total = start[V];
+  const int cut = worker_lo(blockIdx.x + 1, total, G);
+  if (cut >= total) return;
+  const int v = seq_of_block(start, V, cut);
+  const int v0 = start[v], v1 = start[v + 1];
+  if (v0 >= cut) return;                                  // the cut falls between two
+  const int k0 = worker_of(v0, total, G), k1 = worker_of(v1 - 1, total, G);
+  // an empty worker's boundary repeats the one before it
+  if (k0 != (int)blockIdx.x) return;
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
+  const VSeq s = vseq[v];
+  if (s.row0 + r >= s.T * H) return;
+  auto slot = [&](int k) { return (long long)(2 * k + (k == k0 ? 1 : 0)) * 128 + r; };
+  auto has = [&](int k) { return worker_lo(k + 1, total, G) > worker_lo(k, total, G); };
+  float mx = -INFINITY;
+  for (int k = k0; k <= k1; ++k)
+    if (has(k)) mx = fmaxf(mx, ws_lse[slot(k)]);
+  float acc[16];
+#pragma unroll
+  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  float z = 0.f;
+  if (mx != -INFINITY)
+    for (int k = k0; k <= k1; ++k) {
+      if (!has(k)) continue;
+      const float w = __expf(ws_lse[slot(k)] - mx);
+      if (w == 0.f) continue;
+      z += w;
+      const float4* src = reinterpret_cast<const float4*>(ws_o + slot(k) * dtc::kDC);
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 x = src[32 * q + lane];
+        acc[4 * q] = fmaf(w, x.x, acc[4 * q]);
+        acc[4 * q + 1] = fmaf(w, x.y, acc[4 * q + 1]);
+        acc[4 * q + 2] = fmaf(w, x.z, acc[4 * q + 2]);
+        acc[4 * q + 3] = fmaf(w, x.w, acc[4 * q + 3]);
+      }
+    }
+  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const long long row = (long long)s.q0 * H + s.row0 + r;
+  uint2* dst = reinterpret_cast<uint2*>(o + row * dtc::kDC);
+#pragma unroll
+  for (int q = 0; q < 4; ++q)
+    dst[32 * q + lane] = make_uint2(pack_bf16x2(acc[4 * q] * inv, acc[4 * q + 1] * inv),
+                                    pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
+  if (lane == 0) lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
+}
+
+struct ChunkLayout {
+  long long V;
+  int G;
+  size_t off_first, off_vseq, off_lse, off_o, total;
+};
+
+inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
+  auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
+  ChunkLayout c;
+  c.V = chunk_max_v(total_q, B, H);
+  c.G = G;
+  c.off_first = up(sizeof(int32_t) * (c.V + 1));
+  c.off_vseq = c.off_first + up(sizeof(int32_t) * ((size_t)B + 1));
+  c.off_lse = c.off_vseq + up(sizeof(VSeq) * c.V);
+  c.off_o = c.off_lse + up(sizeof(float) * 2 * G * 128);
+  c.total = c.off_o + sizeof(float) * 2 * G * 128 * dtc::kDC;
+  return c;
+}
+
+inline mla_status launch_chunk_tc_impl(
+    bool (*make_tmap)(CUtensorMap*, const void*, int, const uint64_t*, const uint64_t*,
+                      const uint32_t*),
+    const void* qbuf, const int32_t* cu_q, int total_q, int max_q, const void* pool, int n_pages,
+    const int32_t* page_table, int max_pages, const int32_t* seq_lens, int B, int H, float scale,
+    char* ws, const ChunkLayout& c, __nv_bfloat16* o, float* lse, cudaStream_t st) {
+  using namespace dtc;
+  int32_t* start = reinterpret_cast<int32_t*>(ws);
+  int32_t* first = reinterpret_cast<int32_t*>(ws + c.off_first);
+  VSeq* vseq = reinterpret_cast<VSeq*>(ws + c.off_vseq);
+  float* ws_lse = reinterpret_cast<float*>(ws + c.off_lse);
+  float* ws_o = reinterpret_cast<float*>(ws + c.off_o);
+  CUtensorMap tQ, tQK, tPV;
+  if (!decode_tc_tmaps(make_tmap, qbuf, (long long)total_q * H, pool, n_pages, tQ, tQK, tPV))
+    return MLA_ERR_CUDA;
+  if (cudaFuncSetAttribute(decode_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                           (int)kSmemBytes) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  chunk_plan_kernel<<<1, 1024, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
+                                        (int)c.V, first, vseq, start);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  DecodeTcParams p{};
+  p.pool = static_cast<const uint8_t*>(pool);
+  p.page_table = page_table;
+  p.seq_lens = seq_lens;
+  p.start = start;
+  p.ws_lse = ws_lse;
+  p.ws_o = ws_o;
+  p.n_pages = n_pages;
+  p.max_pages = max_pages;
+  p.B = B;
+  p.H = H;
+  p.G = c.G;
+  p.scale_log2 = scale * 1.4426950408889634f;
+  p.vseq = vseq;
+  p.V = (int)c.V;
+  p.o = o;
+  p.lse = lse;
+  decode_tc_kernel<true><<<2 * c.G, kThreads, kSmemBytes, st>>>(tQ, tQK, tPV, p);
+  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  chunk_combine_kernel<<<dim3(c.G, 16), 256, 0, st>>>(ws_lse, ws_o, start, vseq, (int)c.V, H, c.G,
+                                                      o, lse);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace mla

@@ -127,6 +127,17 @@ constexpr uint32_t kTmemS = 256;     // S_b, then P_b, at columns [256 + 128b, +
 constexpr float kRescaleLog2 = 8.0f;
 }  // namespace dtc
 
+// One virtual sequence: up to 128 query rows of a sequence.  The decode has
+// R row blocks of every sequence; a batch of ragged chunks (chunk_tc.cuh) has
+// as many as each chunk fills, listed by its planner.
+struct VSeq {
+  int b;      // sequence
+  int row0;   // its first row, within the rows of the sequence
+  int q0;     // the sequence's first query token
+  int T;      // the sequence's query tokens
+  int L;      // cached tokens it may look at
+};
+
 struct DecodeTcParams {
   const uint8_t* pool;    // [n_pages][64][576] bf16
   const int32_t* page_table;
@@ -137,7 +148,22 @@ struct DecodeTcParams {
   float* ws_o;            // [slots][128][512]
   int n_pages, max_pages, B, S_q, H, R, G;
   float scale_log2;       // softmax scale * log2(e)
+  // ragged chunks only
+  const VSeq* vseq;       // [V]
+  int V;
+  __nv_bfloat16* o;       // [total_q][H][512]
+  float* lse;             // [total_q][H]
 };
+
+template <bool kRagged>
+__device__ __forceinline__ VSeq virtual_seq(const DecodeTcParams& P, int v) {
+  if constexpr (kRagged) {
+    return P.vseq[v];
+  } else {
+    const int b = v % P.B;
+    return VSeq{b, (v / P.B) * 128, b * P.S_q, P.S_q, P.seq_lens[b]};
+  }
+}
 
 __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   uint32_t r;
@@ -195,6 +221,10 @@ __device__ __forceinline__ int page_of(const DecodeTcParams& P, int b, int L, in
   return pg;
 }
 
+// kRagged: virtual sequences come from the list of a batch of ragged chunks, a
+// piece that is all of one writes its rows itself (bf16), and the others go
+// to slot 2 * worker + (the piece opens its virtual sequence).
+template <bool kRagged>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmQ,
                      const __grid_constant__ CUtensorMap tmQK,
@@ -266,11 +296,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
   const uint32_t tmem = tmem_base_sh;
   volatile int* abort_p = &abort_flag;
 
-  const int V = P.B * P.R;
+  const int V = kRagged ? P.V : P.B * P.R;
   const int total = P.start[V];
   const int lo = total > 0 ? worker_lo(worker, total, P.G) : 0;
   const int hi = total > 0 ? worker_lo(worker + 1, total, P.G) : 0;
-  const int rows_seq = P.S_q * P.H;
 
   // Registers: the control warpgroup (producers, MMA) gives up most
   // of its share to the two softmax warpgroups.
@@ -290,15 +319,15 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       int v, x0, x1, piece = 0;
       bool ok = true;
       while (ok && pi.next(v, x0, x1)) {
-        const int b = v % P.B, rb = v / P.B;
-        const int L = P.seq_lens[b];
+        const VSeq vs = virtual_seq<kRagged>(P, v);
+        const int b = vs.b, L = vs.L;
         // the Q slice is free once the previous piece's QK MMAs completed
         if (piece > 0 && !mbar_wait(smem_u32(&q_empty), (piece - 1) & 1, abort_p, 2, piece)) {
           ok = false;
           break;
         }
         if (rank == 0) mbar_expect_tx(smem_u32(&q_full), 2 * kQBytes);
-        const int row0 = b * rows_seq + rb * 128 + 64 * (int)rank;
+        const int row0 = vs.q0 * P.H + vs.row0 + 64 * (int)rank;
         for (int c = 0; c < 9; ++c)
           tma_load_2d_pair(sQ + c * kChunk, &tmQ, c * 64, row0, lead_qfull);
         ++q_issued;
@@ -365,8 +394,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       bool ok = true;
       const int rsub = lane >> 4, cc = (lane >> 3) & 1, u = lane & 7;
       while (ok && pi.next(v, x0, x1)) {
-        const int b = v % P.B;
-        const int L = P.seq_lens[b];
+        const VSeq vs = virtual_seq<kRagged>(P, v);
+        const int b = vs.b, L = vs.L;
         for (int x = x0; x < x1 && ok; ++x)
           for (int p = 0; p < 4 && ok; ++p) {
             const int pg = page_of(P, b, L, x, p);
@@ -560,11 +589,11 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
     int j = 0, pc = 0;
     bool dead = false;
     while (!dead && pi.next(v, x0, x1)) {
-      const int b = v % P.B, rb = v / P.B;
-      const int L = P.seq_lens[b];
-      const int grow = rb * 128 + 64 * (int)rank + h;      // row within the sequence
-      const int tail = P.tail != nullptr ? P.tail[b] : 0;
-      const int limit = min(L, L + tail - P.S_q + grow / P.H + 1);  // visible tokens t < limit
+      const VSeq vs = virtual_seq<kRagged>(P, v);
+      const int L = vs.L;
+      const int grow = vs.row0 + 64 * (int)rank + h;       // row within the sequence
+      const int tail = !kRagged && P.tail != nullptr ? P.tail[vs.b] : 0;
+      const int limit = min(L, L + tail - vs.T + grow / P.H + 1);  // visible tokens t < limit
       float m = -INFINITY, l = 0.f;
       bool o_started = false;
       for (int x = x0; x < x1; ++x, ++j) {
@@ -746,10 +775,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       tc_fence_after();
       const float lt = red_sum[h] + red_sum[64 + h] + red_sum[128 + h] + red_sum[192 + h];
       const float inv = lt > 0.f ? 1.f / lt : 0.f;
-      const long long slot = (long long)worker + v;
-      const long long row = slot * 128 + 64 * (int)rank + h;
       // this warp writes latent half n = ch of its lanes: columns
       // 256n + 128hh + [0, 128)
+      if constexpr (kRagged) {
+        if (x0 == 0 && x1 == P.start[v + 1] - P.start[v]) {
+          // the whole virtual sequence: its rows are final
+          const bool live = grow < vs.T * P.H;
+          const long long row = (long long)vs.q0 * P.H + grow;
+          // All TMEM loads come before the rows part ways: a warp whose last
+          // rows lie past the chunk must not be split when it issues one.
+          uint32_t w[64];
+#pragma unroll
+          for (int cc = 0; cc < 4; ++cc) {
+            uint32_t r[32];
+            tmem_ld32(tmem + lane_addr + kTmemO + 128 * ch + 32 * cc, r);
+            tmem_wait_ld();
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              w[16 * cc + i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv,
+                                           __uint_as_float(r[2 * i + 1]) * inv);
+          }
+          if (live) {
+            uint4* d4 = reinterpret_cast<uint4*>(P.o + row * kDC + 256 * ch + 128 * hh);
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+              d4[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            if (pb == 0)
+              P.lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          }
+          __syncwarp();
+          named_bar_sync(1, kSoftmaxThreads);  // red_sum is rewritten by the next piece
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(lead_oempty);
+          continue;
+        }
+      }
+      const long long slot = kRagged ? 2ll * worker + (x0 == 0 ? 1 : 0) : (long long)worker + v;
+      const long long row = slot * 128 + 64 * (int)rank + h;
       float* dst = P.ws_o + row * kDC + 256 * ch + 128 * hh;
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t r[32];
@@ -779,20 +842,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
   if (warp == 1) tmem_dealloc<2>(tmem, kTmemCols);
 }
 
-// Host launcher: TMA descriptors for the query rows and the page pool.
-inline mla_status launch_decode_tc_impl(
-    bool (*make_tmap)(CUtensorMap*, const void*, int, const uint64_t*, const uint64_t*,
-                      const uint32_t*),
-    const void* qbuf, const void* pool, int n_pages, const int32_t* page_table, int max_pages,
-    const int32_t* seq_lens, const int32_t* tail, int B, int S_q, int H, float scale, int G,
-    const int32_t* start, float* ws_lse, float* ws_o, cudaStream_t st) {
+// TMA descriptors for `rows` query rows and the page pool.
+inline bool decode_tc_tmaps(bool (*make_tmap)(CUtensorMap*, const void*, int, const uint64_t*,
+                                              const uint64_t*, const uint32_t*),
+                            const void* qbuf, long long rows, const void* pool, int n_pages,
+                            CUtensorMap& tQ, CUtensorMap& tQK, CUtensorMap& tPV) {
   using namespace dtc;
-  CUtensorMap tQ, tQK, tPV;
   {
-    const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)B * S_q * H};
+    const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)rows};
     const uint64_t strides[1] = {(uint64_t)kD * 2};
     const uint32_t box[2] = {64, 64};
-    if (!make_tmap(&tQ, qbuf, 2, dims, strides, box)) return MLA_ERR_CUDA;
+    if (!make_tmap(&tQ, qbuf, 2, dims, strides, box)) return false;
   }
   // The pool [n_pages][64 slots][576] seen as (64 columns, 8 slots, 9
   // chunks, 8 slot groups, pages): element (col, s, chunk, g, page) at
@@ -803,7 +863,7 @@ inline mla_status launch_decode_tc_impl(
     const uint64_t strides[4] = {(uint64_t)kD * 2, 128, (uint64_t)kD * 2 * 8,
                                  (uint64_t)kPageBytes};
     const uint32_t box[5] = {64, 8, (uint32_t)kQkCps, 8, 1};
-    if (!make_tmap(&tQK, pool, 5, dims, strides, box)) return MLA_ERR_CUDA;
+    if (!make_tmap(&tQK, pool, 5, dims, strides, box)) return false;
   }
   // The pool seen as (64 columns, pool rows, 9 chunks): a box of two chunks
   // of one page lands as [chunk][64 slots][64 columns], the MN-major operand
@@ -812,9 +872,22 @@ inline mla_status launch_decode_tc_impl(
     const uint64_t dims[3] = {64, (uint64_t)n_pages * kPage, 9};
     const uint64_t strides[2] = {(uint64_t)kD * 2, 128};
     const uint32_t box[3] = {64, (uint32_t)kPage, 2};
-    if (!make_tmap(&tPV, pool, 3, dims, strides, box)) return MLA_ERR_CUDA;
+    if (!make_tmap(&tPV, pool, 3, dims, strides, box)) return false;
   }
-  DecodeTcParams p;
+  return true;
+}
+
+inline mla_status launch_decode_tc_impl(
+    bool (*make_tmap)(CUtensorMap*, const void*, int, const uint64_t*, const uint64_t*,
+                      const uint32_t*),
+    const void* qbuf, const void* pool, int n_pages, const int32_t* page_table, int max_pages,
+    const int32_t* seq_lens, const int32_t* tail, int B, int S_q, int H, float scale, int G,
+    const int32_t* start, float* ws_lse, float* ws_o, cudaStream_t st) {
+  using namespace dtc;
+  CUtensorMap tQ, tQK, tPV;
+  if (!decode_tc_tmaps(make_tmap, qbuf, (long long)B * S_q * H, pool, n_pages, tQ, tQK, tPV))
+    return MLA_ERR_CUDA;
+  DecodeTcParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
   p.page_table = page_table;
   p.seq_lens = seq_lens;
@@ -830,10 +903,10 @@ inline mla_status launch_decode_tc_impl(
   p.R = (S_q * H + 127) / 128;  // the last row block may be padded
   p.G = G;
   p.scale_log2 = scale * 1.4426950408889634f;
-  if (cudaFuncSetAttribute(decode_tc_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+  if (cudaFuncSetAttribute(decode_tc_kernel<false>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
-  decode_tc_kernel<<<2 * G, kThreads, kSmemBytes, st>>>(tQ, tQK, tPV, p);
+  decode_tc_kernel<false><<<2 * G, kThreads, kSmemBytes, st>>>(tQ, tQK, tPV, p);
   return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
 }
 
