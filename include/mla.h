@@ -410,6 +410,31 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
                                int B, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
                                void* stream);
 
+/* Attention weight gathered by the cached tokens ([DF-0] gives the weights;
+ * gathering them is an addition of this library).  With the queries, chunks
+ * and scores s of mla_chunk_attention (a decode step of mla_decode is the
+ * chunk cu_q = 0, S_q, 2 S_q, ..) and lse as that call returned it, for every
+ * token t < L = seq_lens[b] of every sequence:
+ *   w_out[b*stride + t] = keep * w_in[b*stride + t]      (t < L - T_b only)
+ *     + sum over the queries j < T_b that see t and the heads i of
+ *       exp(s_{j,i,t} - lse[cu_q[b] + j, i])
+ * so that w_in describes the cache before the chunk and w_out after it; keep
+ * = 1 gathers, less than 1 forgets.  w_in: device fp32 [B, stride], not read
+ * where it is NULL or keep is 0; w_out: device fp32 [B, stride], may be w_in;
+ * entries from L on are left as they were.  A row with lse = -inf gives
+ * nothing.  Products of bf16 accumulate in fp32, the sums are fp32 in a fixed
+ * order (the same bits every time).  Shapes, checks and cu_q as for
+ * mla_chunk_attention; stride >= every length, keep finite.  A cu_q that
+ * breaks its rules leaves w_out as it was; so does, for its sequence, a
+ * length < T_b or > min(stride, max_pages*page_size); both raise
+ * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as
+ * rows of zeros. */
+mla_status mla_attn_weights(const mla_dims* dims, const void* qbuf, const float* lse,
+                            const int32_t* cu_q, int total_q, int max_q, const void* pool,
+                            int n_pages, const int32_t* page_table, int max_pages,
+                            const int32_t* seq_lens, int B, const float* w_in, float keep,
+                            float* w_out, int stride, void* stream);
+
 /* A6 on bf16 rows, as mla_chunk_attention writes them: mla_out_proj without
  * the conversion.  o_lat: device bf16 [T, H, d_latent], 16-byte aligned;
  * scratch: >= mla_out_proj_bf16_scratch_size bytes.  bf16 only (else
@@ -494,7 +519,9 @@ mla_status mla_get_device_status(void* stream);
  * slice free, 3 MMA operands landed, 4 P ready, 5 O free, 6 query landed,
  * 7 S ready, 8-10 PV done), 21-23 GEMM, 30-39 prefill attention (30 value
  * stage free, 31 key stage free, 32 query landed, 33 keys landed, 34 P ready,
- * 35 values landed, 36 S buffer free, 37 S ready, 38-39 PV done).  Reads and clears the record
+ * 35 values landed, 36 S buffer free, 37 S ready, 38-39 PV done), 40-45
+ * gathered weights (40 resident operand free, 41 stage free, 42 resident
+ * operand landed, 43 S buffer free, 44 stage landed, 45 S ready).  Reads and clears the record
  * (synchronous copy; call after mla_get_device_status). */
 mla_status mla_get_wait_diag(uint32_t* out4);
 

@@ -31,7 +31,7 @@ EXPORTS = ("mla_project", "mla_absorb_q", "mla_rope", "mla_cache_append",
            "mla_cache_append_fp8", "mla_cache_quantize_fp8", "mla_decode_fp8",
            "mla_decode_fp8_workspace_size", "mla_prefill_rebuild_kv", "mla_prefill_attention",
            "mla_chunk_attention_workspace_size", "mla_chunk_attention",
-           "mla_out_proj_bf16_scratch_size", "mla_out_proj_bf16",
+           "mla_attn_weights", "mla_out_proj_bf16_scratch_size", "mla_out_proj_bf16",
            "mla_norm_rope", "mla_cache_evict_workspace_size", "mla_cache_evict")
 
 
@@ -118,6 +118,8 @@ _SIGS = {
     "mla_chunk_attention_workspace_size": ([ctypes.POINTER(Dims), _I, _I, _I], _Z),
     "mla_chunk_attention": ([ctypes.POINTER(Dims), _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P, _Z,
                              _P, _P, _P], _I),
+    "mla_attn_weights": ([ctypes.POINTER(Dims), _P, _P, _P, _I, _I, _P, _I, _P, _I, _P, _I, _P,
+                          ctypes.c_float, _P, _I, _P], _I),
     "mla_out_proj_bf16_scratch_size": ([ctypes.POINTER(Dims), _I], _Z),
     "mla_out_proj_bf16": ([ctypes.POINTER(Dims), _P, _P, _P, _P, _Z, _P, _I, _P], _I),
     "mla_norm_rope": ([ctypes.POINTER(Dims), _P, _I, _P, _P, _P, ctypes.c_float, _P, _P, _P, _P,
@@ -373,6 +375,25 @@ def mla_chunk_attention(dims: MLADims, qbuf, cu_q, total_q, max_q, pool, n_pages
         _here(dev, "workspace", workspace, torch.uint8, 0), workspace.numel(),
         _here(dev, "o_lat", o_lat, dt, total_q * H * dims.d_latent),
         _here(dev, "lse", lse, torch.float32, total_q * H),
+        torch._C._cuda_getCurrentRawStream(dev)))
+
+
+def mla_attn_weights(dims: MLADims, qbuf, lse, cu_q, total_q, max_q, pool, n_pages, page_table,
+                     max_pages, seq_lens, B, w_in, keep, w_out, stride):
+    """Attention weight that the cached tokens receive from a chunk's queries, added to keep times
+    what they had gathered before it (w_in, or None); lse as mla_decode or mla_chunk_attention
+    returned it (include/mla.h)."""
+    dev = torch.cuda.current_device()
+    dt, i32, f32 = dims.torch_dtype, torch.int32, torch.float32
+    H, D = dims.n_heads, dims.d_latent + dims.d_rope
+    _check("mla_attn_weights", lib().mla_attn_weights(
+        _ref(dims), _here(dev, "qbuf", qbuf, dt, total_q * H * D),
+        _here(dev, "lse", lse, f32, total_q * H), _here(dev, "cu_q", cu_q, i32, B + 1), total_q,
+        max_q, _here(dev, "pool", pool, dt, n_pages * dims.page_size * D), n_pages,
+        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
+        _here(dev, "seq_lens", seq_lens, i32, B), B,
+        None if w_in is None else _here(dev, "w_in", w_in, f32, B * stride), keep,
+        _here(dev, "w_out", w_out, f32, B * stride), stride,
         torch._C._cuda_getCurrentRawStream(dev)))
 
 

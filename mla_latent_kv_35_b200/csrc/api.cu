@@ -21,6 +21,7 @@
 #include "norm_rope.cuh"
 #include "prefill_tc.cuh"
 #include "simt.cuh"
+#include "weights_tc.cuh"
 
 using namespace mla;
 
@@ -895,6 +896,44 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
       B, dims->n_heads, dims->scale, static_cast<char*>(workspace), c,
       static_cast<__nv_bfloat16*>(o_lat), lse, as_stream(stream));
   g_launches.fetch_add(3, std::memory_order_relaxed);
+  return s;
+}
+
+mla_status mla_attn_weights(const mla_dims* dims, const void* qbuf, const float* lse,
+                            const int32_t* cu_q, int total_q, int max_q, const void* pool,
+                            int n_pages, const int32_t* page_table, int max_pages,
+                            const int32_t* seq_lens, int B, const float* w_in, float keep,
+                            float* w_out, int stride, void* stream) {
+  if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 || max_pages < 1 ||
+      (long long)max_pages * dims->page_size > 0x7FFFFFFFll || stride < 1 || !std::isfinite(keep))
+    return MLA_ERR_INVALID_ARG;
+  if (!chunk_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
+  if (B == 0) return MLA_OK;
+  if (!cu_q || !pool || !page_table || !seq_lens || !w_out || (total_q > 0 && (!qbuf || !lse)))
+    return MLA_ERR_INVALID_ARG;
+  if (!aligned16(qbuf) || !aligned16(pool)) return MLA_ERR_INVALID_ARG;
+  WeightsParams p{};
+  p.lse = lse; p.cu_q = cu_q; p.page_table = page_table; p.seq_lens = seq_lens;
+  p.w_in = w_in; p.w_out = w_out;
+  p.stride = stride;
+  p.total_q = total_q; p.max_q = max_q;
+  p.max_tokens = max_pages * dims->page_size; p.max_pages = max_pages; p.n_pages = n_pages;
+  p.B = B; p.H = dims->n_heads;
+  p.scale_log2 = dims->scale * 1.4426950408889634f;
+  p.keep = keep;
+  const long long rows = (long long)total_q * dims->n_heads;
+  // without query tokens the kernel loads no query rows; the map only has to
+  // be encodable
+  const void* q = total_q > 0 ? qbuf : pool;
+  const long long map_rows = total_q > 0 ? rows : 1;
+  const long long widest = (long long)max_q * dims->n_heads;   // query rows of a sequence
+  const int pairs = sm_count() / 2;
+  cudaStream_t st = as_stream(stream);
+  const mla_status s =
+      widest <= 128   ? launch_weights<true, 128>(make_tmap_bf16, q, map_rows, pool, p, pairs, st)
+      : widest <= 256 ? launch_weights<true, 256>(make_tmap_bf16, q, map_rows, pool, p, pairs, st)
+                      : launch_weights<false, 256>(make_tmap_bf16, q, map_rows, pool, p, pairs, st);
+  g_launches.fetch_add(1, std::memory_order_relaxed);
   return s;
 }
 

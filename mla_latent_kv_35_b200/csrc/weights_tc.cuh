@@ -1,0 +1,487 @@
+// weights_tc.cuh -- the attention weight that every cached token receives from
+// the queries of a chunk (tcgen05 pair MMAs, TMEM accumulators, TMA).
+//
+// What it computes: with s = scale * q . row the scores of mla_decode or
+// mla_chunk_attention, and lse what that call returned,
+//   w_out[b, t] = keep * w_in[b, t] + sum over the queries j and heads i of
+//                 sequence b that see t of exp(s_{j,i,t} - lse_{j,i})
+// (w_in read for the tokens cached before the chunk).  The softmax's
+// denominators are known, so one pass without running maxima does it: a
+// product of the cache rows with the queries, exponentials, and a sum over
+// the queries.
+//
+// Scores are formed with the tokens as the M dimension: S[token, query row]
+// lands in TMEM with one token per lane, so the sum over query rows is a sum
+// over a thread's own columns, and nothing is exchanged between lanes.  A
+// pair of SMs takes 256 tokens (cta_group::2, M = 256): CTA r holds tokens
+// [128 r, 128 r + 128) of them (two pages) as its half of A and half of the
+// query rows as its half of B.
+//
+// Two forms, by which operand stays in shared memory:
+//   kQStat: all query rows of a sequence (at most kN = 128 or 256: decode
+//     and speculative steps) stay, and the cache streams past them, 16 KB
+//     stages of 128 tokens x 64 columns.  Every cache row is read once from
+//     HBM: bound by memory.
+//   otherwise: 256 tokens stay (147 KB per SM) and the query rows stream past
+//     them, 256 at a time, from L2: bound by the tensor pipe.  A token tile
+//     belongs to one pair for all its rows, so the sum needs no second pass
+//     and its order is fixed.
+// Work: the tiles of all sequences laid end to end, each weighing the row
+// blocks it meets, cut into one contiguous run per pair.  Every CTA finds its
+// run itself (a scan over the sequences), so there is no planning launch and
+// no workspace.
+//
+// Row sums: four chains per thread over 32 columns at a time, fp32.  Rows
+// whose lse is not finite give nothing (a query that saw nothing has -inf).
+// Tokens past a sequence's end compute on whatever the page holds there and
+// are not stored.
+//
+// Every mbarrier wait is bounded as in the decode kernel.
+#pragma once
+
+#include "common.cuh"
+#include "decode_tc.cuh"
+#include "chunk_tc.cuh"
+
+namespace mla {
+
+namespace wtc {
+constexpr int kD = 576;
+constexpr int kPage = 64;
+constexpr int kTile = 256;                      // tokens per pair
+constexpr int kTileBytes = 9 * 128 * 128;       // this CTA's 128 tokens x 576 columns (147 KB)
+constexpr int kThreads = 384;
+constexpr int kEpiWarp0 = 4;
+constexpr int kEpiThreads = 256;
+constexpr uint32_t kTmemCols = 512;
+constexpr int kMaxStages = 9;
+template <bool kQStat, int kN>
+struct Shape {
+  static constexpr int kStat = kQStat ? 9 * (kN / 2) * 128 : kTileBytes;       // stationary bytes
+  static constexpr int kStage = kQStat ? 128 * 128 : (kN / 2) * 128;            // 64 columns
+  static constexpr int kStages = kStat > 100 * 1024 ? 4 : 9;
+  static constexpr int kBufs = (int)kTmemCols / kN;                             // S buffers
+  static constexpr uint32_t kSmem = kStat + kStages * kStage + 1024;
+};
+}  // namespace wtc
+
+struct WeightsParams {
+  const float* lse;            // [total_q][H]
+  const int32_t* cu_q;         // [B + 1]
+  const int32_t* page_table;
+  const int32_t* seq_lens;
+  const float* w_in;           // [B][stride], or nullptr
+  float* w_out;                // [B][stride]
+  long long stride;
+  int total_q, max_q, max_tokens, max_pages, n_pages, B, H;
+  float scale_log2, keep;
+};
+
+// Row blocks that a tile of sequence b meets, and whether the sequence is
+// sound.
+template <int kN>
+__device__ __forceinline__ int weights_cost(const WeightsParams& P, int b, int& tiles) {
+  const int T = P.cu_q[b + 1] - P.cu_q[b], L = P.seq_lens[b];
+  const bool ok = T >= 0 && L >= T && L <= P.max_tokens && L <= P.stride;
+  tiles = ok ? (L + wtc::kTile - 1) / wtc::kTile : 0;
+  return max(1, (int)(((long long)T * P.H + kN - 1) / kN));
+}
+
+template <bool kQStat, int kN>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
+    attn_weights_kernel(const __grid_constant__ CUtensorMap tmQ,
+                        const __grid_constant__ CUtensorMap tmK, const WeightsParams P) {
+  using namespace wtc;
+  using S = Shape<kQStat, kN>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], stat_full, stat_empty;
+  __shared__ __align__(8) uint64_t s_full[4], s_free[4], drain;
+  __shared__ __align__(16) float lse2_sh[2][kN];
+  __shared__ __align__(16) int lim_sh[2][kN];
+  __shared__ float red[2][128];
+  __shared__ long long sums[kThreads / 32], run_sh[3];
+  __shared__ uint32_t tmem_base_sh;
+  __shared__ int abort_flag;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t rank = cluster_ctarank();
+  const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t sStat = base, sRing = base + S::kStat;
+
+  if (threadIdx.x == 0) {
+    abort_flag = 0;
+    for (int s = 0; s < S::kStages; ++s) {
+      mbar_init(smem_u32(&full[s]), 1);      // the leader's arrive with both CTAs' bytes
+      mbar_init(smem_u32(&empty[s]), 1);     // MMA commit (both CTAs)
+    }
+    mbar_init(smem_u32(&stat_full), 1);
+    mbar_init(smem_u32(&stat_empty), 1);
+    for (int b = 0; b < S::kBufs; ++b) {
+      mbar_init(smem_u32(&s_full[b]), 1);    // MMA commit (both CTAs)
+      mbar_init(smem_u32(&s_free[b]), 16);   // 8 epilogue warps x 2 CTAs
+    }
+    mbar_init(smem_u32(&drain), 1);
+    fence_mbar_init();
+    tma_prefetch_desc(&tmQ);
+    tma_prefetch_desc(&tmK);
+    run_sh[0] = P.B;
+    run_sh[1] = 0;
+    run_sh[2] = 0;
+  }
+  if (warp == 1) {
+    tmem_alloc<2>(smem_u32(&tmem_base_sh), kTmemCols);
+    tmem_relinquish<2>();
+  }
+
+  // ---- this pair's run: first sequence, first tile, cost at its end ----
+  bool wrong = false;
+  long long mine = 0;
+  for (int b = threadIdx.x; b < P.B; b += kThreads) {
+    wrong |= chunk_bad(P.cu_q, b, P.total_q, P.max_q);
+    int tiles;
+    const int c = weights_cost<kN>(P, b, tiles);
+    mine += (long long)tiles * (kQStat ? 1 : c);
+    if (blockIdx.x == 0 && (P.seq_lens[b] < P.cu_q[b + 1] - P.cu_q[b] ||
+                            P.seq_lens[b] > P.max_tokens || P.seq_lens[b] > P.stride))
+      raise_flag(kFlagBounds);
+  }
+  if (__syncthreads_or(wrong)) {
+    if (blockIdx.x == 0 && threadIdx.x == 0) raise_flag(kFlagBounds);
+    mine = 0;
+    wrong = true;
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) mine += __shfl_xor_sync(0xffffffffu, mine, o);
+  if (lane == 0) sums[warp] = mine;
+  __syncthreads();
+  long long total = 0;
+#pragma unroll
+  for (int w = 0; w < kThreads / 32; ++w) total += sums[w];
+  const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
+  const long long lo = total * pair / pairs, hi = total * (pair + 1) / pairs;
+  // tiles whose first row block's place in the whole lies in [lo, hi)
+  if (hi > lo) {
+    long long before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
+      const int b = b0 + threadIdx.x;
+      int tiles = 0, c = 1;
+      if (b < P.B) c = weights_cost<kN>(P, b, tiles);
+      if (kQStat) c = 1;
+      const long long x = (long long)tiles * c;
+      long long inc = x;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      __syncthreads();
+      if (lane == 31) sums[warp] = inc;
+      __syncthreads();
+      long long at = before + inc - x, all = 0;
+#pragma unroll
+      for (int w = 0; w < kThreads / 32; ++w) {
+        at += w < warp ? sums[w] : 0;
+        all += sums[w];
+      }
+      // the first tile at or past lo: in this sequence, or at the start of a
+      // later one
+      if (x > 0 && at <= lo && lo < at + x) {
+        const long long t = (lo - at + c - 1) / c;
+        run_sh[0] = t < tiles ? b : b + 1;
+        run_sh[1] = t < tiles ? t : 0;
+        run_sh[2] = t < tiles ? at + t * c : at + x;
+      }
+      before += all;
+    }
+  }
+  tc_fence_before();
+  cluster_sync();
+  tc_fence_after();
+  const uint32_t tmem = tmem_base_sh;
+  volatile int* abort_p = &abort_flag;
+
+  // Every role walks the same tiles: sequences from run_sh on, tiles in
+  // order, until the cost reaches hi.
+  struct Walk {
+    int b, x, tiles, T, L, q0, blocks;
+    long long cost, hi;
+  };
+  auto walk_seq = [&](Walk& w) {
+    // skip to a sequence with tiles left; false at the end of the run
+    while (w.b < P.B && w.cost < w.hi) {
+      w.blocks = weights_cost<kN>(P, w.b, w.tiles);
+      if (w.x < w.tiles) {
+        w.q0 = P.cu_q[w.b];
+        w.T = P.cu_q[w.b + 1] - w.q0;
+        w.L = P.seq_lens[w.b];
+        if (w.T == 0) w.blocks = 0;
+        return true;
+      }
+      ++w.b;
+      w.x = 0;
+    }
+    return false;
+  };
+  Walk w0;
+  w0.b = (int)run_sh[0];
+  w0.x = (int)run_sh[1];
+  w0.cost = run_sh[2];
+  w0.hi = hi > lo ? hi : 0;
+  auto tile_cost = [&](const Walk& w) { return kQStat ? 1 : max(1, w.blocks); };
+  // page holding tokens 64 i of this CTA's half of tile x, or n_pages (out
+  // of bounds: the box reads zeros)
+  auto page_at = [&](const Walk& w, int i) {
+    const int t0 = w.x * kTile + 128 * (int)rank + 64 * i;
+    if (t0 >= w.L) return P.n_pages;
+    const int pg = P.page_table[(long long)w.b * P.max_pages + t0 / kPage];
+    if (pg < 0 || pg >= P.n_pages) {
+      raise_flag(kFlagBounds);
+      return P.n_pages;
+    }
+    return pg;
+  };
+
+  if (warp == 0 && lane == 0) {
+    // =====================  producer (both CTAs)  =====================
+    const uint32_t lead_full0 = mapa_shared(smem_u32(&full[0]), rank & ~1u);
+    const uint32_t lead_stat = mapa_shared(smem_u32(&stat_full), rank & ~1u);
+    uint32_t it = 0, stats = 0;
+    bool ok = true;
+    Walk w = w0;
+    int loaded = -1;                       // sequence whose rows are stationary
+    while (ok && walk_seq(w)) {
+      if (w.blocks > 0) {
+        const int pg0 = page_at(w, 0), pg1 = page_at(w, 1);
+        auto load_tile_chunk = [&](uint32_t dst, int c, uint32_t bar) {
+          tma_load_3d_pair(dst, &tmK, 0, pg0 * kPage, c, bar);
+          tma_load_3d_pair(dst + 8192, &tmK, 0, pg1 * kPage, c, bar);
+        };
+        if (!kQStat || loaded != w.b) {
+          // (the stationary operand is free once the MMAs on it completed)
+          if (stats > 0 && !mbar_wait(smem_u32(&stat_empty), (stats - 1) & 1, abort_p, 40, stats)) {
+            ok = false;
+            break;
+          }
+          if (rank == 0) mbar_expect_tx(smem_u32(&stat_full), 2 * S::kStat);
+          for (int c = 0; c < 9; ++c) {
+            if constexpr (kQStat)
+              tma_load_2d_pair(sStat + c * (kN / 2) * 128, &tmQ, 64 * c,
+                               w.q0 * P.H + (kN / 2) * (int)rank, lead_stat);
+            else
+              load_tile_chunk(sStat + c * 16384, c, lead_stat);
+          }
+          ++stats;
+          loaded = w.b;
+        }
+        const int steps = kQStat ? 1 : w.blocks;
+        for (int rb = 0; rb < steps && ok; ++rb)
+          for (int c = 0; c < 9; ++c, ++it) {
+            const int s = it % S::kStages;
+            if (!mbar_wait(smem_u32(&empty[s]), ((it / S::kStages) & 1) ^ 1, abort_p, 41, it)) {
+              ok = false;
+              break;
+            }
+            const uint32_t fb = lead_full0 + 8 * s;
+            if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * S::kStage);
+            if constexpr (kQStat)
+              load_tile_chunk(sRing + s * S::kStage, c, fb);
+            else
+              tma_load_2d_pair(sRing + s * S::kStage, &tmQ, 64 * c,
+                               w.q0 * P.H + rb * kN + (kN / 2) * (int)rank, fb);
+          }
+      }
+      w.cost += tile_cost(w);
+      ++w.x;
+    }
+    if (!ok && rank == 0) {
+      // leaving early: wait (bounded) for the copies already armed
+      if (stats > 0) mbar_wait_bounded(smem_u32(&stat_full), (stats - 1) & 1, kDrainNs);
+      for (uint32_t i = it > (uint32_t)S::kStages ? it - S::kStages : 0u; i < it; ++i)
+        mbar_wait_bounded(smem_u32(&full[i % S::kStages]), (i / S::kStages) & 1, kDrainNs);
+    }
+  } else if (warp == 1 && lane == 0 && rank == 0) {
+    // =====================  MMA issuer (leader)  =====================
+    const uint32_t idesc = idesc_bf16_f32(256, kN, false, false);
+    const uint64_t stat_desc = sw128_desc(sStat, 16, 1024);
+    const uint64_t ring_desc = sw128_desc(sRing, 16, 1024);
+    uint32_t it = 0, stats = 0, j = 0;
+    bool ok = true;
+    Walk w = w0;
+    int loaded = -1;
+    while (ok && walk_seq(w)) {
+      const int b = w.b;
+      if (w.blocks > 0) {
+        if (!kQStat || loaded != b) {
+          ok = mbar_wait(smem_u32(&stat_full), stats & 1, abort_p, 42, stats);
+          ++stats;
+          loaded = b;
+        }
+        const int steps = kQStat ? 1 : w.blocks;
+        for (int rb = 0; rb < steps && ok; ++rb, ++j) {
+          const int buf = j % S::kBufs;
+          if (j >= (uint32_t)S::kBufs &&
+              !mbar_wait(smem_u32(&s_free[buf]), (j / S::kBufs - 1) & 1, abort_p, 43, j)) {
+            ok = false;
+            break;
+          }
+          for (int c = 0; c < 9; ++c, ++it) {
+            const int s = it % S::kStages;
+            if (!mbar_wait(smem_u32(&full[s]), (it / S::kStages) & 1, abort_p, 44, it)) {
+              ok = false;
+              break;
+            }
+            tc_fence_after();
+            const uint64_t st = stat_desc + (uint64_t)((c * (S::kStat / 9)) >> 4);
+            const uint64_t ri = ring_desc + (uint64_t)((s * S::kStage) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss<2>(tmem + kN * buf, (kQStat ? ri : st) + 2 * kk,
+                             (kQStat ? st : ri) + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+            mma_commit_2_mc(smem_u32(&empty[s]), 3);
+          }
+          if (ok) mma_commit_2_mc(smem_u32(&s_full[buf]), 3);
+        }
+      }
+      w.cost += tile_cost(w);
+      ++w.x;
+      if (ok && loaded == b && (!kQStat || w.x >= w.tiles)) {
+        mma_commit_2_mc(smem_u32(&stat_empty), 3);
+        loaded = -1;
+      }
+    }
+    if (!ok) {
+      mma_commit_2_mc(smem_u32(&drain), 1);
+      mbar_wait_bounded(smem_u32(&drain), 0, kDrainNs);
+    }
+  } else if (warp >= kEpiWarp0) {
+    // =====================  epilogue (both CTAs)  =====================
+    const int ew = warp - kEpiWarp0;
+    const int quad = ew & 3, ch = ew >> 2;            // TMEM lane quadrant, column half
+    const int tl = 32 * quad + lane;                  // token of this CTA = TMEM lane
+    const int et = threadIdx.x - 32 * kEpiWarp0;      // 0 .. 255
+    const uint32_t lane_addr = (uint32_t)(32 * quad) << 16;
+    const uint32_t lead_free = mapa_shared(smem_u32(&s_free[0]), 0);
+    uint32_t j = 0, refresh = 0, done = 0;
+    int loaded = -1;
+    // Every warp takes every barrier; a wait that gave up only marks the warp,
+    // and the next barrier tells all of them to leave together.
+    bool dead = false, leave = false;
+    Walk w = w0;
+    while (!leave && walk_seq(w)) {
+      const int t = w.x * kTile + 128 * (int)rank + tl;
+      const int steps = kQStat ? min(1, w.blocks) : w.blocks;
+      float acc = 0.f;
+      for (int rb = 0; rb < steps; ++rb, ++j) {
+        // the rows' lse (in units of log2; +inf for a row that gives nothing)
+        // and visible limits.  Two sets in turn: the barrier of the next
+        // refresh keeps a set from being rewritten while it is read.
+        if (!kQStat || loaded != w.b) {
+          const int rows = w.T * P.H - rb * kN;
+          for (int r = et; r < kN; r += kEpiThreads) {
+            float v = INFINITY;
+            int lim = 0;
+            if (r < rows) {
+              const float x = P.lse[(long long)w.q0 * P.H + rb * kN + r];
+              if (x > -INFINITY) v = x * 1.4426950408889634f;
+              lim = w.L - w.T + (rb * kN + r) / P.H + 1;
+            }
+            lse2_sh[refresh & 1][r] = v;
+            lim_sh[refresh & 1][r] = lim;
+          }
+          ++refresh;
+          loaded = w.b;
+          leave = named_bar_or(1, kEpiThreads, dead || *abort_p != 0);
+          if (leave) break;
+        }
+        const float* l2 = lse2_sh[(refresh - 1) & 1] + (kN / 2) * ch;
+        const int* lim = lim_sh[(refresh - 1) & 1] + (kN / 2) * ch;
+        const int buf = j % S::kBufs;
+        const bool got = mbar_wait(smem_u32(&s_full[buf]), (j / S::kBufs) & 1, abort_p, 45, j);
+        if (!__all_sync(0xffffffffu, got)) {
+          dead = true;
+          continue;
+        }
+        tc_fence_after();
+        const uint32_t sa = tmem + lane_addr + kN * buf + (kN / 2) * ch;
+        float s4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int g = 0; g < kN / 64; ++g) {
+          uint32_t r[32];
+          __syncwarp();
+          tmem_ld32(sa + 32 * g, r);
+          tmem_wait_ld();
+#pragma unroll
+          for (int c = 0; c < 32; c += 4) {
+            const float4 l = *reinterpret_cast<const float4*>(l2 + 32 * g + c);
+            const int4 m = *reinterpret_cast<const int4*>(lim + 32 * g + c);
+            const float p0 = ex2_approx(fmaf(__uint_as_float(r[c]), P.scale_log2, -l.x));
+            const float p1 = ex2_approx(fmaf(__uint_as_float(r[c + 1]), P.scale_log2, -l.y));
+            const float p2 = ex2_approx(fmaf(__uint_as_float(r[c + 2]), P.scale_log2, -l.z));
+            const float p3 = ex2_approx(fmaf(__uint_as_float(r[c + 3]), P.scale_log2, -l.w));
+            s4[0] += t < m.x && l.x < INFINITY ? p0 : 0.f;
+            s4[1] += t < m.y && l.y < INFINITY ? p1 : 0.f;
+            s4[2] += t < m.z && l.z < INFINITY ? p2 : 0.f;
+            s4[3] += t < m.w && l.w < INFINITY ? p3 : 0.f;
+          }
+        }
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(lead_free + 8 * buf);
+        acc += (s4[0] + s4[1]) + (s4[2] + s4[3]);
+      }
+      if (leave) break;
+      // the two column halves meet; one thread per token stores
+      if (ch == 1) red[done & 1][tl] = acc;
+      leave = named_bar_or(2, kEpiThreads, dead || *abort_p != 0);
+      if (leave) break;
+      if (ch == 0 && t < w.L) {
+        const long long i = w.b * P.stride + t;
+        float v = acc + red[done & 1][tl];
+        if (P.w_in != nullptr && P.keep != 0.f && t < w.L - w.T) v = fmaf(P.keep, P.w_in[i], v);
+        P.w_out[i] = v;
+      }
+      ++done;
+      w.cost += tile_cost(w);
+      ++w.x;
+    }
+  }
+
+  // =====================  teardown  =====================
+  __syncwarp();
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();
+  if (warp == 1) tmem_dealloc<2>(tmem, kTmemCols);
+}
+
+template <bool kQStat, int kN>
+inline mla_status launch_weights(bool (*make_tmap)(CUtensorMap*, const void*, int, const uint64_t*,
+                                                   const uint64_t*, const uint32_t*),
+                                 const void* qbuf, long long rows, const void* pool,
+                                 const WeightsParams& p, int pairs, cudaStream_t st) {
+  using namespace wtc;
+  CUtensorMap tQ, tK;
+  {
+    const uint64_t dims[2] = {(uint64_t)kD, (uint64_t)rows};
+    const uint64_t strides[1] = {(uint64_t)kD * 2};
+    const uint32_t box[2] = {64, kN / 2};
+    if (!make_tmap(&tQ, qbuf, 2, dims, strides, box)) return MLA_ERR_CUDA;
+  }
+  // the pool as (64 columns, pool rows, 9 chunks): a box is one page's slots
+  // of one chunk
+  {
+    const uint64_t dims[3] = {64, (uint64_t)p.n_pages * kPage, 9};
+    const uint64_t strides[2] = {(uint64_t)kD * 2, 128};
+    const uint32_t box[3] = {64, (uint32_t)kPage, 1};
+    if (!make_tmap(&tK, pool, 3, dims, strides, box)) return MLA_ERR_CUDA;
+  }
+  auto kfn = attn_weights_kernel<kQStat, kN>;
+  constexpr uint32_t smem = Shape<kQStat, kN>::kSmem;
+  if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
+      cudaSuccess)
+    return MLA_ERR_CUDA;
+  kfn<<<2 * pairs, kThreads, smem, st>>>(tQ, tK, p);
+  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+}
+
+}  // namespace mla
