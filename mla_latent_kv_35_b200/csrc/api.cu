@@ -1037,8 +1037,12 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   a.stride = stride;
   a.max_tokens = max_pages * dims->page_size;
   a.n_sink = n_sink; a.n_recent = n_recent;
+  // the fewest blocks whose threads hold a sequence's keys, and more while
+  // that leaves SMs idle and a block has more than 4096 slots
   int cluster = 1;
-  while (cluster < kEvictMaxCluster && stride > (long long)kEvictSlotsPerBlock * cluster)
+  while (cluster < kEvictMaxCluster &&
+         (stride > (long long)kEvictSlots * cluster ||
+          (stride > 4096LL * cluster && 2LL * B * cluster <= sm_count())))
     cluster *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(B * cluster));
@@ -1051,22 +1055,26 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, evict_plan_kernel, a) != cudaSuccess) return MLA_ERR_CUDA;
+  auto plan = stride <= (long long)kEvictSlots * cluster ? evict_plan_kernel<true>
+                                                         : evict_plan_kernel<false>;
+  if (cudaLaunchKernelEx(&cfg, plan, a) != cudaSuccess) return MLA_ERR_CUDA;
   MLA_TRY(check_launch());
   const long long row_bytes = fp8_rows ? fp8::kRowBytes
                                        : (long long)(dims->d_latent + dims->d_rope) *
                                              (dims->dtype == MLA_F32 ? 4 : 2);
-  // about eight blocks per SM over all sequences
-  const long long x = (8LL * sm_count() + B - 1) / B;
-  dim3 grid((unsigned)std::min<long long>(x, ((long long)stride + 7) / 8), (unsigned)B);
+  // at most eight blocks per SM, no more warps than pairs
+  const unsigned grid = (unsigned)std::min<long long>(
+      8LL * sm_count(), ((long long)B * stride / 2 + 7) / 8 + 1);
   if (row_bytes % 16 == 0 && aligned16(pool))
     evict_move_kernel<uint4><<<grid, 256, 0, st>>>(
         static_cast<uint4*>(pool), (int)(row_bytes / 16), n_pages, dims->page_size, page_table,
-        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, stride);
+        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, B,
+        stride);
   else
     evict_move_kernel<uint16_t><<<grid, 256, 0, st>>>(
         static_cast<uint16_t*>(pool), (int)(row_bytes / 2), n_pages, dims->page_size, page_table,
-        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, stride);
+        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, B,
+        stride);
   return check_launch();
 }
 

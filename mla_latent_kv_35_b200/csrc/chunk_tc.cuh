@@ -70,13 +70,24 @@ __device__ __forceinline__ bool chunk_bad(const int32_t* cu_q, int b, int total_
 // of their token blocks.  A cu_q that breaks its rules anywhere gives no
 // blocks at all: chunks could overlap.  A sequence whose length is impossible
 // keeps its rows with nothing to see (one empty block), so that they come out
-// as 0 and -inf.  first: [B + 1], scratch.
+// as 0 and -inf.  first: [B + 1], scratch for B > kPlanSeqs.  cuts[k], k <
+// G - 1: the virtual sequence that the boundary between workers k and k + 1
+// cuts (-1: none), with its first and last worker.
+constexpr int kPlanSeqs = 2048;
+struct ChunkCut {
+  int v, k0, k1, pad;
+};
 __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
                                                           const int32_t* seq_lens, int B, int H,
                                                           int total_q, int max_q, int max_tokens,
-                                                          int V, int32_t* first, VSeq* vseq,
-                                                          int32_t* start) {
+                                                          int V, int G, int32_t* first_global,
+                                                          VSeq* vseq, int32_t* start,
+                                                          ChunkCut* cuts) {
   __shared__ int warp_sums[32];
+  __shared__ int first_sh[kPlanSeqs + 1];
+  pdl_launch();
+  int32_t* first = B <= kPlanSeqs ? first_sh : first_global;
+  for (int k = threadIdx.x; k < G; k += 1024) cuts[k].v = -1;
   bool wrong = false;
   for (int b = threadIdx.x; b < B; b += 1024) wrong |= chunk_bad(cu_q, b, total_q, max_q);
   if (__syncthreads_or(wrong)) {
@@ -124,68 +135,95 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
     blocks += sum;
   }
   if (threadIdx.x == 0) start[V] = blocks;
+  __syncthreads();
+  const int workers = min(G, blocks);
+  for (int v = threadIdx.x; v < live; v += 1024) {
+    const int v0 = start[v], v1 = start[v + 1];
+    if (v1 <= v0) continue;
+    const int k0 = worker_of(v0, blocks, workers), k1 = worker_of(v1 - 1, blocks, workers);
+    for (int k = k0; k < k1; ++k) cuts[k] = ChunkCut{v, k0, k1, 0};
+  }
 }
 
-// Merges the virtual sequences that worker boundaries cut.  Block (k, y)
-// looks at the boundary between workers k and k + 1: if it is the first one
-// inside its virtual sequence, the block's eight warps merge rows 8y .. 8y +
-// 7 of it, a warp per row.
+// Merges the virtual sequences that worker boundaries cut, by log-sum-exp.  A
+// virtual sequence cut into n pieces has n - 1 boundaries, each with 16
+// blocks; its 128 rows go 8, 4, 2 or 1 to a block, so that few pieces use few
+// blocks and many pieces (a long context with few queries) all of them.  The
+// 8 / rows warps of a row take its pieces in turn and meet in shared memory;
+// a lane owns four float4 columns.
 __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse, const float* ws_o,
-                                                            const int32_t* start, const VSeq* vseq,
-                                                            int V, int H, int G, __nv_bfloat16* o,
-                                                            float* lse) {
-  const int total = start[V];
-  const int cut = worker_lo(blockIdx.x + 1, total, G);
-  if (cut >= total) return;
-  const int v = seq_of_block(start, V, cut);
-  const int v0 = start[v], v1 = start[v + 1];
-  if (v0 >= cut) return;                                  // the cut falls between two
-  const int k0 = worker_of(v0, total, G), k1 = worker_of(v1 - 1, total, G);
-  // an empty worker's boundary repeats the one before it
-  if (k0 != (int)blockIdx.x) return;
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5);
-  const VSeq s = vseq[v];
-  if (s.row0 + r >= s.T * H) return;
-  auto slot = [&](int k) { return (long long)(2 * k + (k == k0 ? 1 : 0)) * 128 + r; };
-  auto has = [&](int k) { return worker_lo(k + 1, total, G) > worker_lo(k, total, G); };
+                                                            const ChunkCut* cuts, const VSeq* vseq,
+                                                            int H, __nv_bfloat16* o, float* lse) {
+  __shared__ float4 part[8][128];
+  pdl_wait();
+  const ChunkCut c = cuts[blockIdx.x];
+  if (c.v < 0) return;
+  const int n = c.k1 - c.k0 + 1;
+  const int blocks = 16 * (n - 1);
+  const int rows = blocks >= 128 ? 1 : blocks >= 64 ? 2 : blocks >= 32 ? 4 : 8;
+  const int first = ((int)(blockIdx.x - c.k0) * 16 + (int)blockIdx.y) * rows;
+  if (first >= 128) return;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int wpr = 8 / rows, u = w % wpr;
+  const int r = first + w / wpr;
+  const VSeq s = vseq[c.v];
+  const bool live = s.row0 + r < s.T * H;
+  // piece i: worker k0 + i; the first opens the virtual sequence
+  auto slot = [&](int i) { return (long long)(2 * (c.k0 + i) + (i == 0 ? 1 : 0)) * 128 + r; };
   float mx = -INFINITY;
-  for (int k = k0; k <= k1; ++k)
-    if (has(k)) mx = fmaxf(mx, ws_lse[slot(k)]);
-  float acc[16];
+  for (int i = lane; i < n; i += 32) mx = fmaxf(mx, ws_lse[slot(i)]);
 #pragma unroll
-  for (int i = 0; i < 16; ++i) acc[i] = 0.f;
+  for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
   float z = 0.f;
-  if (mx != -INFINITY)
-    for (int k = k0; k <= k1; ++k) {
-      if (!has(k)) continue;
-      const float w = __expf(ws_lse[slot(k)] - mx);
-      if (w == 0.f) continue;
-      z += w;
-      const float4* src = reinterpret_cast<const float4*>(ws_o + slot(k) * dtc::kDC);
+  float4 acc[4];
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (mx != -INFINITY && live) {
+    for (int i = lane; i < n; i += 32) z += __expf(ws_lse[slot(i)] - mx);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+#pragma unroll 2
+    for (int i = u; i < n; i += wpr) {
+      const float e = __expf(ws_lse[slot(i)] - mx);
+      const float4* src = reinterpret_cast<const float4*>(ws_o + slot(i) * dtc::kDC);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const float4 x = src[32 * q + lane];
-        acc[4 * q] = fmaf(w, x.x, acc[4 * q]);
-        acc[4 * q + 1] = fmaf(w, x.y, acc[4 * q + 1]);
-        acc[4 * q + 2] = fmaf(w, x.z, acc[4 * q + 2]);
-        acc[4 * q + 3] = fmaf(w, x.w, acc[4 * q + 3]);
+        acc[q].x = fmaf(e, x.x, acc[q].x);
+        acc[q].y = fmaf(e, x.y, acc[q].y);
+        acc[q].z = fmaf(e, x.z, acc[q].z);
+        acc[q].w = fmaf(e, x.w, acc[q].w);
       }
     }
+  }
+  if (wpr > 1) {
+    if (u != 0)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) part[w][32 * q + lane] = acc[q];
+    __syncthreads();
+    if (u != 0) return;
+    for (int t = 1; t < wpr; ++t)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const float4 y = part[w + t][32 * q + lane];
+        acc[q].x += y.x; acc[q].y += y.y; acc[q].z += y.z; acc[q].w += y.w;
+      }
+  }
+  if (!live) return;
   const float inv = z > 0.f ? 1.f / z : 0.f;
   const long long row = (long long)s.q0 * H + s.row0 + r;
   uint2* dst = reinterpret_cast<uint2*>(o + row * dtc::kDC);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
-    dst[32 * q + lane] = make_uint2(pack_bf16x2(acc[4 * q] * inv, acc[4 * q + 1] * inv),
-                                    pack_bf16x2(acc[4 * q + 2] * inv, acc[4 * q + 3] * inv));
+    dst[32 * q + lane] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv),
+                                    pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
   if (lane == 0) lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
 }
 
 struct ChunkLayout {
   long long V;
   int G;
-  size_t off_first, off_vseq, off_lse, off_o, total;
+  size_t off_first, off_vseq, off_cuts, off_lse, off_o, total;
 };
 
 inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
@@ -195,7 +233,8 @@ inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
   c.G = G;
   c.off_first = up(sizeof(int32_t) * (c.V + 1));
   c.off_vseq = c.off_first + up(sizeof(int32_t) * ((size_t)B + 1));
-  c.off_lse = c.off_vseq + up(sizeof(VSeq) * c.V);
+  c.off_cuts = c.off_vseq + up(sizeof(VSeq) * c.V);
+  c.off_lse = c.off_cuts + up(sizeof(ChunkCut) * G);
   c.off_o = c.off_lse + up(sizeof(float) * 2 * G * 128);
   c.total = c.off_o + sizeof(float) * 2 * G * 128 * dtc::kDC;
   return c;
@@ -211,6 +250,7 @@ inline mla_status launch_chunk_tc_impl(
   int32_t* start = reinterpret_cast<int32_t*>(ws);
   int32_t* first = reinterpret_cast<int32_t*>(ws + c.off_first);
   VSeq* vseq = reinterpret_cast<VSeq*>(ws + c.off_vseq);
+  ChunkCut* cuts = reinterpret_cast<ChunkCut*>(ws + c.off_cuts);
   float* ws_lse = reinterpret_cast<float*>(ws + c.off_lse);
   float* ws_o = reinterpret_cast<float*>(ws + c.off_o);
   CUtensorMap tQ, tQK, tPV;
@@ -220,7 +260,7 @@ inline mla_status launch_chunk_tc_impl(
                            (int)kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
   chunk_plan_kernel<<<1, 1024, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
-                                        (int)c.V, first, vseq, start);
+                                        (int)c.V, c.G, first, vseq, start, cuts);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   DecodeTcParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
@@ -239,11 +279,27 @@ inline mla_status launch_chunk_tc_impl(
   p.V = (int)c.V;
   p.o = o;
   p.lse = lse;
-  decode_tc_kernel<true><<<2 * c.G, kThreads, kSmemBytes, st>>>(tQ, tQK, tPV, p);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
-  chunk_combine_kernel<<<dim3(c.G, 16), 256, 0, st>>>(ws_lse, ws_o, start, vseq, (int)c.V, H, c.G,
-                                                      o, lse);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  // both may start while their predecessor runs: the attention sets up its
+  // barriers and TMEM under the plan
+  cudaLaunchAttribute pdl[1];
+  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  pdl[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(2 * c.G);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = st;
+  cfg.attrs = pdl;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, decode_tc_kernel<true>, tQ, tQK, tPV, p) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  cfg.gridDim = dim3(c.G, 16);
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  if (cudaLaunchKernelEx(&cfg, chunk_combine_kernel, (const float*)ws_lse, (const float*)ws_o,
+                         (const ChunkCut*)cuts, (const VSeq*)vseq, H, o, lse) != cudaSuccess)
+    return MLA_ERR_CUDA;
+  return MLA_OK;
 }
 
 }  // namespace mla

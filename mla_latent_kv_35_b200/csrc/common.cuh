@@ -176,6 +176,17 @@ __device__ __forceinline__ void cluster_sync() {
                    : "memory");
 }
 
+// Programmatic dependent launch: a kernel launched with the attribute may
+// start before its predecessor has finished.  pdl_wait returns once the
+// predecessor is complete and its writes are visible; pdl_launch lets the
+// successor start.
+__device__ __forceinline__ void pdl_wait() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
+__device__ __forceinline__ void pdl_launch() {
+  asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---------------------------------------------------------------------------
 // TMA (bulk tensor copies global -> shared)
 // ---------------------------------------------------------------------------

@@ -296,10 +296,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
   const uint32_t tmem = tmem_base_sh;
   volatile int* abort_p = &abort_flag;
 
+  if constexpr (kRagged) {
+    pdl_wait();      // the plan
+    pdl_launch();
+  }
   const int V = kRagged ? P.V : P.B * P.R;
   const int total = P.start[V];
-  const int lo = total > 0 ? worker_lo(worker, total, P.G) : 0;
-  const int hi = total > 0 ? worker_lo(worker + 1, total, P.G) : 0;
+  // (ragged: no more workers than blocks, so that none is empty)
+  const int G = kRagged ? min(P.G, total) : P.G;
+  const int lo = total > 0 && worker < G ? worker_lo(worker, total, G) : 0;
+  const int hi = total > 0 && worker < G ? worker_lo(worker + 1, total, G) : 0;
 
   // Registers: the control warpgroup (producers, MMA) gives up most
   // of its share to the two softmax warpgroups.

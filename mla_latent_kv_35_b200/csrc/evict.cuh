@@ -17,19 +17,24 @@
 //     11, 11 and 10 bits find the n_out-th smallest key: a histogram of the
 //     digit in shared memory, summed over the cluster's blocks through
 //     distributed shared memory, then a scan for the digit that holds the
-//     rank.  Nothing is sorted.
-//   * Among equal keys the lowest slots leave.  Every warp owns one run of
-//     consecutive slots and walks it with ballots, so ranks within a run need
-//     no barrier; the runs' counts meet in two scans per block and one
-//     exchange per cluster.
+//     rank.  Nothing is sorted.  The first pass's sum is the number of free
+//     slots, so it needs no count of its own.
+//   * Every warp owns one run of consecutive slots, 32 at a time, and keeps
+//     their keys in registers (kCached: up to 16 per thread, 131072 slots in
+//     a cluster of 8; beyond that each pass reads the weights again).  Ranks
+//     within a run come from ballots; the runs' counts meet in one scan per
+//     block and one exchange per cluster.
+//   * Among equal keys the lowest slots leave.  Their ranks take another
+//     exchange, made only where some of the equal ones stay.
 //   * It writes the pairs (vacated slot, moving slot), the survivors' weights
 //     and positions that stay where they are, and the new length.
-// evict_move_kernel: a warp per pair copies the row, its weight and its
-// position.
+// evict_move_kernel: every warp takes an even share of all sequences' pairs
+// and copies row, weight and position, two rows in flight.  (A grid of blocks
+// per sequence left the SMs of the short ones idle: 115 us against 40 for 64
+// ragged sequences.)
 //
-// Bound: the plan by latency (six walks over a block's part of the weights,
-// the later ones from L1, and four cluster barriers), the move by memory
-// bandwidth.
+// Bound: the plan by latency (loads, then three to six cluster barriers), the
+// move by memory bandwidth.
 #pragma once
 
 #include "common.cuh"
@@ -39,8 +44,9 @@ namespace mla {
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictMaxCluster = 8;
 constexpr int kEvictBins = 2048;
-// slots per block from which a sequence gets another block
-constexpr int kEvictSlotsPerBlock = 4096;
+constexpr int kEvictKeys = 16;                              // keys a thread can hold
+constexpr int kEvictSlots = kEvictKeys * kEvictThreads;     // slots a block can hold
+constexpr int kEvictGroups = 2048;                          // sequence groups of the move
 
 struct EvictArgs {
   const int32_t* seq_lens;
@@ -77,6 +83,20 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// The pair of words at `addr` in every block of the cluster (zeros past the
+// n-th), all loads in flight at once: one remote read takes about 600 clocks.
+__device__ __forceinline__ void ld_cluster_all(uint32_t addr, uint32_t n,
+                                               int2 (&v)[kEvictMaxCluster]) {
+#pragma unroll
+  for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
+    v[r] = make_int2(0, 0);
+    if (r < n)
+      asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];"
+                   : "=r"(v[r].x), "=r"(v[r].y)
+                   : "r"(mapa_shared(addr, r)));
+  }
+}
+
 __device__ __forceinline__ int warp_inclusive(int x, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -87,40 +107,43 @@ __device__ __forceinline__ int warp_inclusive(int x, int lane) {
 }
 
 // Exclusive prefix over the warps of the cluster's blocks, in slot order, of
-// one count per warp; *total receives the sum.  Every thread of the cluster
-// calls it; cell is a shared word that no other call of the kernel uses.
+// one pair of counts per warp; *total receives the sums.  Every thread of the
+// cluster calls it, each call with a cell of its own.
 struct EvictScan {
-  int warp_sum[32];
-  int block_sum;
+  int2 warp_sum[32];
+  __align__(8) int2 block_sum;
 };
-__device__ __forceinline__ int evict_scan(EvictScan* sc, int count, int warp, int lane,
-                                          uint32_t rank, uint32_t n, int* total) {
+__device__ __forceinline__ int2 evict_scan(EvictScan* sc, int2 count, int warp, int lane,
+                                           uint32_t rank, uint32_t n, int2* total) {
   if (lane == 0) sc->warp_sum[warp] = count;
   __syncthreads();
-  const int mine = sc->warp_sum[lane];
-  const int inc = warp_inclusive(mine, lane);
-  const int before = __shfl_sync(0xffffffffu, inc - mine, warp);
-  const int all = __shfl_sync(0xffffffffu, inc, 31);
-  if (n == 1) {
-    *total = all;
-    return before;
-  }
-  if (threadIdx.x == 0) sc->block_sum = all;
+  const int2 mine = sc->warp_sum[lane];
+  const int ix = warp_inclusive(mine.x, lane), iy = warp_inclusive(mine.y, lane);
+  int2 before = make_int2(__shfl_sync(0xffffffffu, ix - mine.x, warp),
+                          __shfl_sync(0xffffffffu, iy - mine.y, warp));
+  *total = make_int2(__shfl_sync(0xffffffffu, ix, 31), __shfl_sync(0xffffffffu, iy, 31));
+  if (n == 1) return before;
+  if (threadIdx.x == 0) sc->block_sum = *total;
   cluster_sync();
-  int base = 0, sum = 0;
-  for (uint32_t r = 0; r < n; ++r) {
-    const int v = ld_cluster(smem_u32(&sc->block_sum), r);
-    base += r < rank ? v : 0;
-    sum += v;
+  int2 sum = make_int2(0, 0), v[kEvictMaxCluster];
+  ld_cluster_all(smem_u32(&sc->block_sum), n, v);
+#pragma unroll
+  for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
+    before.x += r < rank ? v[r].x : 0;
+    before.y += r < rank ? v[r].y : 0;
+    sum.x += v[r].x;
+    sum.y += v[r].y;
   }
   *total = sum;
-  return base + before;
+  return before;
 }
 
+template <bool kCached>
 __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictArgs a) {
-  __shared__ int hist[3][kEvictBins];        // one per pass: no barrier to reuse it
-  __shared__ EvictScan scan_free, scan_eq, scan_hole, scan_move;
-  __shared__ int digit_sh, below_sh, max_sh;
+  __shared__ __align__(8) int hist[3][kEvictBins];   // one per pass: no barrier to reuse it
+  __shared__ EvictScan scan_eq, scan_out;
+  __shared__ int warp_sums[32];
+  __shared__ int digit_sh, below_sh, here_sh, max_sh;
   const uint32_t n = cluster_nctas(), rank = cluster_ctarank();
   const int b = blockIdx.x / n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -129,61 +152,100 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   const float* w = a.weights + b * a.stride;
   const int32_t* sp = a.slot_pos != nullptr ? a.slot_pos + b * a.stride : nullptr;
   const int Lc = bad ? 0 : L;
+  const int over = max(Lc - max(a.budget[b], 0), 0);     // slots above the budget
   // this warp's run of slots: a multiple of 32 for every warp
-  const int run = ((Lc + (int)n * 1024 - 1) / ((int)n * 1024)) * 32;
+  const int run = ((Lc + (int)n * kEvictThreads - 1) / ((int)n * kEvictThreads)) * 32;
   const int s0 = min(Lc, ((int)rank * 32 + warp) * run), s1 = min(Lc, s0 + run);
-  for (int i = threadIdx.x; i < 3 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
-  if (threadIdx.x == 0) max_sh = -1;
-  __syncthreads();
+  const int groups = (s1 - s0 + 31) / 32;                // of 32 slots
 
-  // ---- the end of the positions, and how many slots are free ----
-  int end = Lc;
-  if (sp != nullptr) {
-    int mx = -1;
-    for (int t = s0 + lane; t < s1; t += 32) mx = max(mx, sp[t]);
-    mx = __reduce_max_sync(0xffffffffu, mx);
-    if (lane == 0) atomicMax(&max_sh, mx);
-    if (n > 1) {
-      cluster_sync();
-      mx = -1;
-      for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
-    } else {
-      __syncthreads();
-      mx = max_sh;
-    }
-    end = mx + 1;
-  }
-  const int p1 = end - a.n_recent;   // free positions: [n_sink, p1)
-  auto is_free = [&](int t) {
+  // keys of this thread's slots s0 + 32 i + lane, and bit i of `free_bits`
+  // where that slot is free
+  uint32_t key[kCached ? kEvictKeys : 1];
+  uint32_t free_bits = 0;
+  int p1 = Lc - a.n_recent;              // free positions: [n_sink, p1)
+  auto free_at = [&](int t) {
     const int p = sp != nullptr ? sp[t] : t;
     return p >= a.n_sink && p < p1;
   };
-  int n_free = 0;
-  if (sp != nullptr) {
-    int c = 0;
-    for (int t = s0; t < s1; t += 32)
-      c += __popc(__ballot_sync(0xffffffffu, t + lane < s1 && is_free(t + lane)));
-    evict_scan(&scan_free, c, warp, lane, rank, n, &n_free);
-  } else {
-    n_free = max(0, p1 - a.n_sink);
-  }
-  const int n_out = min(max(Lc - max(a.budget[b], 0), 0), n_free);
-  const int new_len = Lc - n_out;
+  // f(i, key, free) over this thread's groups; key and free of a slot past the
+  // run are 0 and false
+  auto each = [&](auto f) {
+    if constexpr (kCached) {
+#pragma unroll
+      for (int i = 0; i < kEvictKeys; ++i)
+        if (i < groups) f(i, key[i], (free_bits >> i & 1) != 0);
+    } else {
+      for (int i = 0; i < groups; ++i) {
+        const int t = s0 + 32 * i + lane;
+        f(i, t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t));
+      }
+    }
+  };
 
-  // ---- the n_out-th smallest key, digit by digit ----
-  uint32_t prefix = 0;      // digits found so far
-  int need = n_out;         // rank among the keys with that prefix, from 1
-  if (n_out > 0) {
+  int n_out = 0, need = 0, n_hole = 0;
+  uint32_t kth = 0;       // key of the last slot to leave; `need` slots with it leave
+  if (over > 0) {
+    for (int i = threadIdx.x; i < 3 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
+    if (threadIdx.x == 0) max_sh = -1;
+    int mx = -1;
+    if constexpr (kCached) {
+      // all loads first (a slot past the run reads the run's last one), so
+      // that they are in flight together
+      int pos[kEvictKeys];
+#pragma unroll
+      for (int i = 0; i < kEvictKeys; ++i) {
+        key[i] = 0;
+        if (i < groups) key[i] = __float_as_uint(w[min(s0 + 32 * i + lane, s1 - 1)]);
+      }
+#pragma unroll
+      for (int i = 0; i < kEvictKeys; ++i) {
+        const int t = min(s0 + 32 * i + lane, s1 - 1);
+        pos[i] = t;
+        if (sp != nullptr && i < groups) pos[i] = sp[t];
+      }
+#pragma unroll
+      for (int i = 0; i < kEvictKeys; ++i) {
+        const bool in = s0 + 32 * i + lane < s1;
+        key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
+        pos[i] = in ? pos[i] : -1;
+        mx = max(mx, pos[i]);
+      }
+      __syncthreads();
+      if (sp != nullptr) {
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) atomicMax(&max_sh, mx);
+        if (n > 1) cluster_sync(); else __syncthreads();
+        mx = max_sh;
+        if (n > 1)
+          for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
+        p1 = mx + 1 - a.n_recent;
+      }
+#pragma unroll
+      for (int i = 0; i < kEvictKeys; ++i)
+        if (pos[i] >= max(a.n_sink, 0) && pos[i] < p1) free_bits |= 1u << i;
+    } else {
+      __syncthreads();
+      if (sp != nullptr) {
+        for (int t = s0 + lane; t < s1; t += 32) mx = max(mx, sp[t]);
+        mx = __reduce_max_sync(0xffffffffu, mx);
+        if (lane == 0) atomicMax(&max_sh, mx);
+        if (n > 1) cluster_sync(); else __syncthreads();
+        mx = max_sh;
+        if (n > 1)
+          for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
+        p1 = mx + 1 - a.n_recent;
+      }
+    }
+
+    // ---- the n_out-th smallest key, digit by digit ----
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
-      const int bits = pass == 2 ? 10 : 11;
+      const uint32_t mask = pass == 2 ? 0x3FFu : 0x7FFu;
       const uint32_t known = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-      for (int t = s0 + lane; t < s1; t += 32) {
-        const uint32_t k = evict_key(w[t]);
-        if ((k & known) == prefix && is_free(t))
-          atomicAdd(&hist[pass][(k >> shift) & ((1u << bits) - 1)], 1);
-      }
+      each([&](int, uint32_t k, bool fr) {
+        if (fr && (k & known) == kth) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
+      });
       if (n > 1) cluster_sync(); else __syncthreads();
       // thread i owns bins 2i, 2i + 1
       int c0 = 0, c1 = 0;
@@ -192,90 +254,123 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
         c0 = hist[pass][2 * threadIdx.x];
         c1 = hist[pass][2 * threadIdx.x + 1];
       } else {
-        for (uint32_t r = 0; r < n; ++r) {
-          c0 += ld_cluster(cell, r);
-          c1 += ld_cluster(cell + 4, r);
+        int2 v[kEvictMaxCluster];
+        ld_cluster_all(cell, n, v);
+#pragma unroll
+        for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
+          c0 += v[r].x;
+          c1 += v[r].y;
         }
       }
       const int inc = warp_inclusive(c0 + c1, lane);
-      if (lane == 31) scan_move.warp_sum[warp] = inc;
+      if (lane == 31) warp_sums[warp] = inc;
       __syncthreads();
-      const int ws = scan_move.warp_sum[lane];
+      const int ws = warp_sums[lane];
       const int wi = warp_inclusive(ws, lane);
+      if (pass == 0) {
+        n_out = min(over, __shfl_sync(0xffffffffu, wi, 31));   // the sum: every free slot
+        need = n_out;
+      }
       const int before = __shfl_sync(0xffffffffu, wi - ws, warp) + inc - c0 - c1;
       if (before < need && need <= before + c0 + c1) {
         const bool second = need > before + c0;
         digit_sh = 2 * threadIdx.x + (second ? 1 : 0);
         below_sh = before + (second ? c0 : 0);
+        here_sh = second ? c1 : c0;
       }
       __syncthreads();
-      prefix |= (uint32_t)digit_sh << shift;
+      if (n_out == 0) break;              // (uniform: nothing is free)
+      kth |= (uint32_t)digit_sh << shift;
       need -= below_sh;
     }
   }
-  const uint32_t kth = prefix;   // `need` of the slots with this key leave, the lowest ones
-  __syncthreads();
-
-  // ---- ranks of the equal keys, then of the vacated and the moving slots ----
-  int eq0 = 0, n_eq = 0;
-  if (n_out > 0) {
-    int c = 0;
-    for (int t = s0; t < s1; t += 32) {
-      const int u = t + lane;
-      c += __popc(__ballot_sync(0xffffffffu, u < s1 && evict_key(w[u]) == kth && is_free(u)));
-    }
-    eq0 = evict_scan(&scan_eq, c, warp, lane, rank, n, &n_eq);
-  }
-  // one bit per slot of 32: leaves; eq counts the equal keys before the slots
-  auto leaving = [&](int t, int& eq) {
-    const int u = t + lane;
-    const uint32_t k = u < s1 ? evict_key(w[u]) : 0u;
-    const bool fr = u < s1 && is_free(u);
-    const uint32_t e = __ballot_sync(0xffffffffu, fr && k == kth);
-    const int r = eq + __popc(e & ((1u << lane) - 1));
-    eq += __popc(e);
-    return __ballot_sync(0xffffffffu, fr && (k < kth || (k == kth && r < need)));
+  const int new_len = Lc - n_out;
+  // weight and position of a slot that stays
+  float* nw = a.new_weights != a.weights ? a.new_weights + b * a.stride : nullptr;
+  int32_t* np = a.new_pos != nullptr && a.new_pos != a.slot_pos ? a.new_pos + b * a.stride : nullptr;
+  auto keep_slot = [&](int t) {
+    if (nw != nullptr) nw[t] = w[t];
+    if (np != nullptr) np[t] = sp != nullptr ? sp[t] : t;
   };
-  const int live_end = s1;
-  int n_hole = 0;
-  if (n_out > 0) {
-    int eq = eq0, holes = 0, moves = 0;
-    for (int t = s0; t < s1; t += 32) {
-      const uint32_t out = leaving(t, eq);
-      const uint32_t live = live_end - t >= 32 ? 0xffffffffu : (1u << (live_end - t)) - 1;
-      const uint32_t front = new_len - t >= 32 ? 0xffffffffu
-                             : new_len > t     ? (1u << (new_len - t)) - 1 : 0u;
-      holes += __popc(out & front);
-      moves += __popc(live & ~out & ~front);
-    }
-    int n_move;
-    int hole = evict_scan(&scan_hole, holes, warp, lane, rank, n, &n_hole);
-    int move = evict_scan(&scan_move, moves, warp, lane, rank, n, &n_move);
-    int2* pairs = a.pairs + b * a.stride;
-    const uint32_t lower = (1u << lane) - 1;
-    eq = eq0;
-    for (int t = s0; t < s1; t += 32) {
-      const uint32_t out = leaving(t, eq);
-      const uint32_t live = live_end - t >= 32 ? 0xffffffffu : (1u << (live_end - t)) - 1;
-      const uint32_t front = new_len - t >= 32 ? 0xffffffffu
-                             : new_len > t     ? (1u << (new_len - t)) - 1 : 0u;
-      const uint32_t h = out & front, m = live & ~out & ~front;
-      if (h >> lane & 1) pairs[hole + __popc(h & lower)].x = t + lane;
-      if (m >> lane & 1) pairs[move + __popc(m & lower)].y = t + lane;
-      hole += __popc(h);
-      move += __popc(m);
-      if ((live & front & ~out) >> lane & 1) {
-        if (a.new_weights != a.weights) a.new_weights[b * a.stride + t + lane] = w[t + lane];
-        if (a.new_pos != nullptr && a.new_pos != a.slot_pos)
-          a.new_pos[b * a.stride + t + lane] = sp != nullptr ? sp[t + lane] : t + lane;
+  // those of all slots with a bit in `stay`, four loads in flight
+  auto keep_slots = [&](uint32_t stay) {
+#pragma unroll
+    for (int i0 = 0; i0 < kEvictKeys; i0 += 4) {
+      if (i0 >= groups) break;
+      float v[4];
+      int p[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int t = min(s0 + 32 * (i0 + i) + lane, s1 - 1);
+        v[i] = nw != nullptr ? w[t] : 0.f;
+        p[i] = np != nullptr && sp != nullptr ? sp[t] : t;
       }
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (stay >> (i0 + i) & 1) {
+          const int t = s0 + 32 * (i0 + i) + lane;
+          if (nw != nullptr) nw[t] = v[i];
+          if (np != nullptr) np[t] = p[i];
+        }
     }
+  };
+  const uint32_t lower = (1u << lane) - 1;
+  if (n_out > 0) {
+    // ---- ranks of the equal keys, where some of them stay ----
+    const bool all_equal = need == here_sh;
+    int eq0 = 0;
+    if (!all_equal) {
+      int c = 0;
+      each([&](int, uint32_t k, bool fr) {
+        c += __popc(__ballot_sync(0xffffffffu, fr && k == kth));
+      });
+      int2 sum;
+      eq0 = evict_scan(&scan_eq, make_int2(c, 0), warp, lane, rank, n, &sum).x;
+    }
+    // the slots of group i that leave, as a mask of lanes; eq counts the
+    // equal keys of the groups before it
+    auto leaving = [&](uint32_t k, bool fr, int& eq) {
+      if (all_equal) return __ballot_sync(0xffffffffu, fr && k <= kth);
+      const uint32_t e = __ballot_sync(0xffffffffu, fr && k == kth);
+      const int r = eq + __popc(e & lower);
+      eq += __popc(e);
+      return __ballot_sync(0xffffffffu, fr && (k < kth || (k == kth && r < need)));
+    };
+    // slots of group i before slot `end`, as a mask of lanes
+    auto until = [&](int i, int end) {
+      const int d = end - (s0 + 32 * i);
+      return d >= 32 ? 0xffffffffu : d > 0 ? (1u << d) - 1 : 0u;
+    };
+    // ---- ranks of the vacated and the moving slots ----
+    int eq = eq0;
+    int2 c = make_int2(0, 0);
+    each([&](int i, uint32_t k, bool fr) {
+      const uint32_t out = leaving(k, fr, eq), front = until(i, new_len);
+      c.x += __popc(out & front);
+      c.y += __popc(until(i, s1) & ~out & ~front);
+    });
+    int2 sum, at = evict_scan(&scan_out, c, warp, lane, rank, n, &sum);
+    n_hole = sum.x;
+    int2* pairs = a.pairs + b * a.stride;
+    eq = eq0;
+    uint32_t stay = 0;          // bit i: slot i of this thread stays where it is
+    each([&](int i, uint32_t k, bool fr) {
+      const int t = s0 + 32 * i + lane;
+      const uint32_t out = leaving(k, fr, eq), front = until(i, new_len);
+      const uint32_t h = out & front, m = until(i, s1) & ~out & ~front;
+      if (h >> lane & 1) pairs[at.x + __popc(h & lower)].x = t;
+      if (m >> lane & 1) pairs[at.y + __popc(m & lower)].y = t;
+      at.x += __popc(h);
+      at.y += __popc(m);
+      const bool stays = (until(i, s1) & front & ~out) >> lane & 1;
+      if constexpr (kCached)
+        stay |= (uint32_t)stays << i;
+      else if (stays)
+        keep_slot(t);
+    });
+    if constexpr (kCached) keep_slots(stay);
   } else {
-    for (int t = s0 + lane; t < s1; t += 32) {
-      if (a.new_weights != a.weights) a.new_weights[b * a.stride + t] = w[t];
-      if (a.new_pos != nullptr && a.new_pos != a.slot_pos)
-        a.new_pos[b * a.stride + t] = sp != nullptr ? sp[t] : t;
-    }
+    for (int t = s0 + lane; t < s1; t += 32) keep_slot(t);
   }
   // every block of the cluster has read seq_lens[b] and its peers' shared
   // memory: the length may be overwritten, and the blocks may end
@@ -287,33 +382,110 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   }
 }
 
-// Copies the rows of all pairs: a warp per pair, block (x, b) takes pairs
-// 8x, 8x + 1, .. of sequence b and every 8 gridDim.x-th after them.  U is the
-// widest unit that divides a row (16 or 2 bytes).
+// Moves the rows of all pairs.  The pairs of all sequences laid end to end are
+// cut evenly over the grid's warps.  U is the widest unit that divides a row
+// (16 or 2 bytes).
 template <typename U>
 __global__ void __launch_bounds__(256) evict_move_kernel(
     U* pool, int units, int n_pages, int page_size, const int32_t* page_table, int max_pages,
     const float* weights, const int32_t* slot_pos, float* new_weights, int32_t* new_pos,
-    const int2* pairs, const int32_t* n_pairs, long long stride) {
-  const int b = blockIdx.y, lane = threadIdx.x & 31;
-  const int n = n_pairs[b];
-  const int32_t* pages = page_table + (long long)b * max_pages;
-  for (int i = blockIdx.x * 8 + (threadIdx.x >> 5); i < n; i += gridDim.x * 8) {
-    const int2 p = pairs[b * stride + i];
-    const int pt = pages[p.x / page_size], pf = pages[p.y / page_size];
-    if (pt < 0 || pt >= n_pages || pf < 0 || pf >= n_pages) {
-      if (lane == 0) raise_flag(kFlagBounds);
-    } else {
-      U* to = pool + ((long long)pt * page_size + p.x % page_size) * units;
-      const U* from = pool + ((long long)pf * page_size + p.y % page_size) * units;
-#pragma unroll 4
-      for (int u = lane; u < units; u += 32) to[u] = from[u];
+    const int2* pairs, const int32_t* n_pairs, int B, long long stride) {
+  __shared__ long long before[kEvictGroups + 1];   // pairs before each group of sequences
+  __shared__ long long sums[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int per = (B + kEvictGroups - 1) / kEvictGroups, n_groups = (B + per - 1) / per;
+  long long base = 0;
+  for (int g0 = 0; g0 < n_groups; g0 += 256) {
+    const int g = g0 + threadIdx.x;
+    long long c = 0;
+    for (int b = g * per; g < n_groups && b < min(B, (g + 1) * per); ++b) c += n_pairs[b];
+    long long inc = c;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
     }
-    if (lane == 0) {
-      new_weights[b * stride + p.x] = weights[b * stride + p.y];
-      if (new_pos != nullptr)
-        new_pos[b * stride + p.x] = slot_pos != nullptr ? slot_pos[b * stride + p.y] : p.y;
+    if (lane == 31) sums[warp] = inc;
+    __syncthreads();
+    long long all = 0, front = 0;
+    for (int i = 0; i < 8; ++i) {
+      front += i < warp ? sums[i] : 0;
+      all += sums[i];
     }
+    if (g < n_groups) before[g] = base + front + inc - c;
+    base += all;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) before[n_groups] = base;
+  __syncthreads();
+  const long long warps = (long long)gridDim.x * 8, me = (long long)blockIdx.x * 8 + warp;
+  const long long lo = base * me / warps, hi = base * (me + 1) / warps;
+  if (lo >= hi) return;
+  // the sequence of pair lo
+  int ga = 0, gb = n_groups - 1;
+  while (ga < gb) {
+    const int mid = (ga + gb) >> 1;
+    if (before[mid + 1] > lo) gb = mid; else ga = mid + 1;
+  }
+  int b = ga * per, i = (int)(lo - before[ga]), n = n_pairs[b];
+  while (i >= n) {
+    i -= n;
+    n = n_pairs[++b];
+  }
+  constexpr int kRows = 2;                 // rows in flight
+  for (long long g = lo; g < hi;) {
+    int2 p[kRows];
+    int bb[kRows];
+    U* to[kRows];
+    const U* from[kRows];
+    int live = 0;
+#pragma unroll
+    for (int q = 0; q < kRows; ++q) {
+      to[q] = nullptr;
+      if (g >= hi) continue;
+      while (i >= n) {
+        i = 0;
+        n = n_pairs[++b];
+      }
+      bb[q] = b;
+      p[q] = pairs[b * stride + i];
+      const int32_t* pages = page_table + (long long)b * max_pages;
+      const int pt = pages[p[q].x / page_size], pf = pages[p[q].y / page_size];
+      if (pt < 0 || pt >= n_pages || pf < 0 || pf >= n_pages) {
+        if (lane == 0) raise_flag(kFlagBounds);
+      } else {
+        to[q] = pool + ((long long)pt * page_size + p[q].x % page_size) * units;
+        from[q] = pool + ((long long)pf * page_size + p[q].y % page_size) * units;
+      }
+      ++live;
+      ++i;
+      ++g;
+    }
+    for (int u0 = 0; u0 < units; u0 += 96) {
+      U v[kRows][3];
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int u = u0 + 32 * k + lane;
+          if (q < live && to[q] != nullptr && u < units) v[q][k] = from[q][u];
+        }
+#pragma unroll
+      for (int q = 0; q < kRows; ++q)
+#pragma unroll
+        for (int k = 0; k < 3; ++k) {
+          const int u = u0 + 32 * k + lane;
+          if (q < live && to[q] != nullptr && u < units) to[q][u] = v[q][k];
+        }
+    }
+#pragma unroll
+    for (int q = 0; q < kRows; ++q)
+      if (q < live && lane == q) {
+        const long long d = bb[q] * stride;
+        new_weights[d + p[q].x] = weights[d + p[q].y];
+        if (new_pos != nullptr)
+          new_pos[d + p[q].x] = slot_pos != nullptr ? slot_pos[d + p[q].y] : p[q].y;
+      }
   }
 }
 
