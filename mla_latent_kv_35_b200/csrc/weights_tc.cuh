@@ -26,10 +26,11 @@
 //     them, 256 at a time, from L2: bound by the tensor pipe.  A token tile
 //     belongs to one pair for all its rows, so the sum needs no second pass
 //     and its order is fixed.
-// Work: the tiles of all sequences laid end to end, each weighing the row
-// blocks it meets, cut into one contiguous run per pair.  Every CTA finds its
-// run itself (a scan over the sequences), so there is no planning launch and
-// no workspace.
+// Work: all sequences' tokens laid end to end, cut into one contiguous run per
+// pair: in pages where the queries stay (a run's tiles start at any page, so
+// that runs differ by one page, not by one tile), in whole tiles otherwise,
+// each weighing the row blocks it meets.  Every CTA finds its run itself (a
+// scan over the sequences), so there is no planning launch and no workspace.
 //
 // Row sums: four chains per thread over 32 columns at a time, fp32.  Rows
 // whose lse is not finite give nothing (a query that saw nothing has -inf).
@@ -55,11 +56,18 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 9;
+#ifndef MLA_WEIGHTS_CHUNKS
+#define MLA_WEIGHTS_CHUNKS 3
+#endif
 template <bool kQStat, int kN>
 struct Shape {
   static constexpr int kStat = kQStat ? 9 * (kN / 2) * 128 : kTileBytes;       // stationary bytes
-  static constexpr int kStage = kQStat ? 128 * 128 : (kN / 2) * 128;            // 64 columns
-  static constexpr int kStages = kStat > 100 * 1024 ? 4 : 9;
+  // A stage: kCps 64-column chunks of 128 tokens, or one of kN / 2 query rows.
+  static constexpr int kCps = !kQStat ? 1 : kN == 128 ? MLA_WEIGHTS_CHUNKS : 1;
+  static constexpr int kStage = kQStat ? kCps * 128 * 128 : (kN / 2) * 128;
+  static constexpr int kSteps = (9 + kCps - 1) / kCps;                          // per tile or row block
+  static constexpr int kRing = kStat > 100 * 1024 ? 64 * 1024 : 144 * 1024;
+  static constexpr int kStages = kRing / kStage;
   static constexpr int kBufs = (int)kTmemCols / kN;                             // S buffers
   static constexpr uint32_t kSmem = kStat + kStages * kStage + 1024;
 };
@@ -77,14 +85,16 @@ struct WeightsParams {
   float scale_log2, keep;
 };
 
-// Row blocks that a tile of sequence b meets, and whether the sequence is
-// sound.
-template <int kN>
-__device__ __forceinline__ int weights_cost(const WeightsParams& P, int b, int& tiles) {
+// Units of work of sequence b (0 where its length is impossible): pages where
+// the queries stay, else tiles; returns what a unit weighs: 1, or the row
+// blocks that a tile meets.
+template <bool kQStat, int kN>
+__device__ __forceinline__ int weights_units(const WeightsParams& P, int b, int& units) {
   const int T = P.cu_q[b + 1] - P.cu_q[b], L = P.seq_lens[b];
   const bool ok = T >= 0 && L >= T && L <= P.max_tokens && L <= P.stride;
-  tiles = ok ? (L + wtc::kTile - 1) / wtc::kTile : 0;
-  return max(1, (int)(((long long)T * P.H + kN - 1) / kN));
+  constexpr int kUnit = kQStat ? wtc::kPage : wtc::kTile;
+  units = ok ? (L + kUnit - 1) / kUnit : 0;
+  return kQStat ? 1 : max(1, (int)(((long long)T * P.H + kN - 1) / kN));
 }
 
 template <bool kQStat, int kN>
@@ -136,11 +146,16 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   // ---- this pair's run: first sequence, first tile, cost at its end ----
   bool wrong = false;
   long long mine = 0;
+  int u_first = 0, c_first = 1;          // of the thread's first sequence
   for (int b = threadIdx.x; b < P.B; b += kThreads) {
     wrong |= chunk_bad(P.cu_q, b, P.total_q, P.max_q);
-    int tiles;
-    const int c = weights_cost<kN>(P, b, tiles);
-    mine += (long long)tiles * (kQStat ? 1 : c);
+    int units;
+    const int c = weights_units<kQStat, kN>(P, b, units);
+    mine += (long long)units * c;
+    if (b < kThreads) {
+      u_first = units;
+      c_first = c;
+    }
     if (blockIdx.x == 0 && (P.seq_lens[b] < P.cu_q[b + 1] - P.cu_q[b] ||
                             P.seq_lens[b] > P.max_tokens || P.seq_lens[b] > P.stride))
       raise_flag(kFlagBounds);
@@ -159,15 +174,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   for (int w = 0; w < kThreads / 32; ++w) total += sums[w];
   const int pairs = gridDim.x >> 1, pair = blockIdx.x >> 1;
   const long long lo = total * pair / pairs, hi = total * (pair + 1) / pairs;
-  // tiles whose first row block's place in the whole lies in [lo, hi)
+  // units whose place in the whole lies in [lo, hi)
   if (hi > lo) {
     long long before = 0;
     for (int b0 = 0; b0 < P.B; b0 += kThreads) {
       const int b = b0 + threadIdx.x;
-      int tiles = 0, c = 1;
-      if (b < P.B) c = weights_cost<kN>(P, b, tiles);
-      if (kQStat) c = 1;
-      const long long x = (long long)tiles * c;
+      int units = u_first, c = c_first;
+      if (b0 > 0) {
+        units = 0;
+        if (b < P.B) c = weights_units<kQStat, kN>(P, b, units);
+      }
+      const long long x = (long long)units * c;
       long long inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -183,13 +200,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
         at += w < warp ? sums[w] : 0;
         all += sums[w];
       }
-      // the first tile at or past lo: in this sequence, or at the start of a
+      // the first unit at or past lo: in this sequence, or at the start of a
       // later one
       if (x > 0 && at <= lo && lo < at + x) {
         const long long t = (lo - at + c - 1) / c;
-        run_sh[0] = t < tiles ? b : b + 1;
-        run_sh[1] = t < tiles ? t : 0;
-        run_sh[2] = t < tiles ? at + t * c : at + x;
+        run_sh[0] = t < units ? b : b + 1;
+        run_sh[1] = t < units ? t : 0;
+        run_sh[2] = t < units ? at + t * c : at + x;
       }
       before += all;
     }
@@ -203,37 +220,55 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   // Every role walks the same tiles: sequences from run_sh on, tiles in
   // order, until the cost reaches hi.
   struct Walk {
-    int b, x, tiles, T, L, q0, blocks;
+    int b, x, units;         // sequence, next unit, its units
+    int T, L, q0, blocks;    // its queries, length, first query token, row blocks (0: no queries)
+    int page, pages;         // this tile: first page, pages (1 .. 4)
+    bool last;               // the last tile of this sequence in the run
     long long cost, hi;
   };
-  auto walk_seq = [&](Walk& w) {
-    // skip to a sequence with tiles left; false at the end of the run
-    while (w.b < P.B && w.cost < w.hi) {
-      w.blocks = weights_cost<kN>(P, w.b, w.tiles);
-      if (w.x < w.tiles) {
+  // the next tile; false at the end of the run
+  auto walk_next = [&](Walk& w) {
+    while (w.cost < w.hi && w.b < P.B) {
+      if (w.units < 0) {                       // a new sequence
+        w.blocks = weights_units<kQStat, kN>(P, w.b, w.units);
         w.q0 = P.cu_q[w.b];
         w.T = P.cu_q[w.b + 1] - w.q0;
         w.L = P.seq_lens[w.b];
         if (w.T == 0) w.blocks = 0;
+      }
+      if (w.x < w.units) {
+        if constexpr (kQStat) {
+          w.page = w.x;
+          w.pages = (int)min((long long)min(4, w.units - w.x), w.hi - w.cost);
+          w.x += w.pages;
+          w.cost += w.pages;
+        } else {
+          w.page = 4 * w.x;
+          w.pages = min(4, (w.L + kPage - 1) / kPage - w.page);
+          ++w.x;
+          w.cost += max(1, w.blocks);
+        }
+        w.last = w.x >= w.units;
         return true;
       }
       ++w.b;
       w.x = 0;
+      w.units = -1;
     }
     return false;
   };
   Walk w0;
   w0.b = (int)run_sh[0];
   w0.x = (int)run_sh[1];
+  w0.units = -1;
   w0.cost = run_sh[2];
   w0.hi = hi > lo ? hi : 0;
-  auto tile_cost = [&](const Walk& w) { return kQStat ? 1 : max(1, w.blocks); };
-  // page holding tokens 64 i of this CTA's half of tile x, or n_pages (out
-  // of bounds: the box reads zeros)
+  // pool page of page i (0, 1) of this CTA's half of the tile; -1: the tile
+  // ends before it, n_pages: its id lies outside the pool (the box reads zeros)
   auto page_at = [&](const Walk& w, int i) {
-    const int t0 = w.x * kTile + 128 * (int)rank + 64 * i;
-    if (t0 >= w.L) return P.n_pages;
-    const int pg = P.page_table[(long long)w.b * P.max_pages + t0 / kPage];
+    const int k = 2 * (int)rank + i;
+    if (k >= w.pages) return -1;
+    const int pg = P.page_table[(long long)w.b * P.max_pages + w.page + k];
     if (pg < 0 || pg >= P.n_pages) {
       raise_flag(kFlagBounds);
       return P.n_pages;
@@ -247,14 +282,31 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     const uint32_t lead_stat = mapa_shared(smem_u32(&stat_full), rank & ~1u);
     uint32_t it = 0, stats = 0;
     bool ok = true;
-    Walk w = w0;
     int loaded = -1;                       // sequence whose rows are stationary
-    while (ok && walk_seq(w)) {
+    // the next tile is looked up while this one loads: page ids take as long
+    // as a box
+    Walk next = w0;
+    int npg0 = 0, npg1 = 0;
+    bool more = walk_next(next);
+    if (more && next.blocks > 0) {
+      npg0 = page_at(next, 0);
+      npg1 = page_at(next, 1);
+    }
+    while (ok && more) {
+      const Walk w = next;
+      const int pg0 = npg0, pg1 = npg1;
+      more = walk_next(next);
+      if (more && next.blocks > 0) {
+        npg0 = page_at(next, 0);
+        npg1 = page_at(next, 1);
+      }
       if (w.blocks > 0) {
-        const int pg0 = page_at(w, 0), pg1 = page_at(w, 1);
+        // the leader arms a barrier with both CTAs' bytes: a page past the
+        // tile is not loaded (its rows compute on what the stage held)
+        const uint32_t tile_bytes = (uint32_t)w.pages * S::kCps * 8192;
         auto load_tile_chunk = [&](uint32_t dst, int c, uint32_t bar) {
-          tma_load_3d_pair(dst, &tmK, 0, pg0 * kPage, c, bar);
-          tma_load_3d_pair(dst + 8192, &tmK, 0, pg1 * kPage, c, bar);
+          if (pg0 >= 0) tma_load_5d_pair(dst, &tmK, 0, 0, c, 0, pg0, bar);
+          if (pg1 >= 0) tma_load_5d_pair(dst + S::kCps * 8192, &tmK, 0, 0, c, 0, pg1, bar);
         };
         if (!kQStat || loaded != w.b) {
           // (the stationary operand is free once the MMAs on it completed)
@@ -262,7 +314,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
             ok = false;
             break;
           }
-          if (rank == 0) mbar_expect_tx(smem_u32(&stat_full), 2 * S::kStat);
+          if (rank == 0)
+            mbar_expect_tx(smem_u32(&stat_full), kQStat ? 2 * S::kStat : 9 * tile_bytes);
           for (int c = 0; c < 9; ++c) {
             if constexpr (kQStat)
               tma_load_2d_pair(sStat + c * (kN / 2) * 128, &tmQ, 64 * c,
@@ -275,23 +328,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
         }
         const int steps = kQStat ? 1 : w.blocks;
         for (int rb = 0; rb < steps && ok; ++rb)
-          for (int c = 0; c < 9; ++c, ++it) {
+          for (int c = 0; c < S::kSteps; ++c, ++it) {
             const int s = it % S::kStages;
             if (!mbar_wait(smem_u32(&empty[s]), ((it / S::kStages) & 1) ^ 1, abort_p, 41, it)) {
               ok = false;
               break;
             }
             const uint32_t fb = lead_full0 + 8 * s;
-            if (rank == 0) mbar_expect_tx(smem_u32(&full[s]), 2 * S::kStage);
+            if (rank == 0)
+              mbar_expect_tx(smem_u32(&full[s]), kQStat ? tile_bytes : 2 * S::kStage);
             if constexpr (kQStat)
-              load_tile_chunk(sRing + s * S::kStage, c, fb);
+              load_tile_chunk(sRing + s * S::kStage, S::kCps * c, fb);
             else
               tma_load_2d_pair(sRing + s * S::kStage, &tmQ, 64 * c,
                                w.q0 * P.H + rb * kN + (kN / 2) * (int)rank, fb);
           }
       }
-      w.cost += tile_cost(w);
-      ++w.x;
     }
     if (!ok && rank == 0) {
       // leaving early: wait (bounded) for the copies already armed
@@ -303,12 +355,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     // =====================  MMA issuer (leader)  =====================
     const uint32_t idesc = idesc_bf16_f32(256, kN, false, false);
     const uint64_t stat_desc = sw128_desc(sStat, 16, 1024);
-    const uint64_t ring_desc = sw128_desc(sRing, 16, 1024);
+    // a page's box lands as [8 slot groups][kCps chunks][8 slots][128 B]
+    const uint64_t ring_desc = sw128_desc(sRing, 16, 1024 * S::kCps);
     uint32_t it = 0, stats = 0, j = 0;
     bool ok = true;
     Walk w = w0;
     int loaded = -1;
-    while (ok && walk_seq(w)) {
+    while (ok && walk_next(w)) {
       const int b = w.b;
       if (w.blocks > 0) {
         if (!kQStat || loaded != b) {
@@ -324,27 +377,30 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
             ok = false;
             break;
           }
-          for (int c = 0; c < 9; ++c, ++it) {
+          for (int k = 0; k < S::kSteps; ++k, ++it) {
             const int s = it % S::kStages;
             if (!mbar_wait(smem_u32(&full[s]), (it / S::kStages) & 1, abort_p, 44, it)) {
               ok = false;
               break;
             }
             tc_fence_after();
-            const uint64_t st = stat_desc + (uint64_t)((c * (S::kStat / 9)) >> 4);
-            const uint64_t ri = ring_desc + (uint64_t)((s * S::kStage) >> 4);
 #pragma unroll
-            for (int kk = 0; kk < 4; ++kk)
-              mma_bf16_ss<2>(tmem + kN * buf, (kQStat ? ri : st) + 2 * kk,
-                             (kQStat ? st : ri) + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+            for (int cc = 0; cc < S::kCps; ++cc) {
+              const int c = k * S::kCps + cc;
+              if (c >= 9) break;               // past the 576 columns
+              const uint64_t st = stat_desc + (uint64_t)((c * (S::kStat / 9)) >> 4);
+              const uint64_t ri = ring_desc + (uint64_t)((s * S::kStage + cc * 1024) >> 4);
+#pragma unroll
+              for (int kk = 0; kk < 4; ++kk)
+                mma_bf16_ss<2>(tmem + kN * buf, (kQStat ? ri : st) + 2 * kk,
+                               (kQStat ? st : ri) + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+            }
             mma_commit_2_mc(smem_u32(&empty[s]), 3);
           }
           if (ok) mma_commit_2_mc(smem_u32(&s_full[buf]), 3);
         }
       }
-      w.cost += tile_cost(w);
-      ++w.x;
-      if (ok && loaded == b && (!kQStat || w.x >= w.tiles)) {
+      if (ok && loaded == b && (!kQStat || w.last)) {
         mma_commit_2_mc(smem_u32(&stat_empty), 3);
         loaded = -1;
       }
@@ -367,8 +423,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     // and the next barrier tells all of them to leave together.
     bool dead = false, leave = false;
     Walk w = w0;
-    while (!leave && walk_seq(w)) {
-      const int t = w.x * kTile + 128 * (int)rank + tl;
+    while (!leave && walk_next(w)) {
+      const int k = 2 * (int)rank + (tl >> 6);           // page of the tile
+      const int t = (w.page + k) * kPage + (tl & 63);
       const int steps = kQStat ? min(1, w.blocks) : w.blocks;
       float acc = 0.f;
       for (int rb = 0; rb < steps; ++rb, ++j) {
@@ -434,15 +491,13 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       if (ch == 1) red[done & 1][tl] = acc;
       leave = named_bar_or(2, kEpiThreads, dead || *abort_p != 0);
       if (leave) break;
-      if (ch == 0 && t < w.L) {
+      if (ch == 0 && k < w.pages && t < w.L) {
         const long long i = w.b * P.stride + t;
         float v = acc + red[done & 1][tl];
         if (P.w_in != nullptr && P.keep != 0.f && t < w.L - w.T) v = fmaf(P.keep, P.w_in[i], v);
         P.w_out[i] = v;
       }
       ++done;
-      w.cost += tile_cost(w);
-      ++w.x;
     }
   }
 
@@ -467,13 +522,14 @@ inline mla_status launch_weights(bool (*make_tmap)(CUtensorMap*, const void*, in
     const uint32_t box[2] = {64, kN / 2};
     if (!make_tmap(&tQ, qbuf, 2, dims, strides, box)) return MLA_ERR_CUDA;
   }
-  // the pool as (64 columns, pool rows, 9 chunks): a box is one page's slots
-  // of one chunk
+  // the pool as (64 columns, 8 slots, 9 chunks, 8 slot groups, pages), as the
+  // decode reads it: a box is kCps chunks of one page
   {
-    const uint64_t dims[3] = {64, (uint64_t)p.n_pages * kPage, 9};
-    const uint64_t strides[2] = {(uint64_t)kD * 2, 128};
-    const uint32_t box[3] = {64, (uint32_t)kPage, 1};
-    if (!make_tmap(&tK, pool, 3, dims, strides, box)) return MLA_ERR_CUDA;
+    const uint64_t dims[5] = {64, 8, 9, 8, (uint64_t)p.n_pages};
+    const uint64_t strides[4] = {(uint64_t)kD * 2, 128, (uint64_t)kD * 2 * 8,
+                                 (uint64_t)kPage * kD * 2};
+    const uint32_t box[5] = {64, 8, (uint32_t)Shape<kQStat, kN>::kCps, 8, 1};
+    if (!make_tmap(&tK, pool, 5, dims, strides, box)) return MLA_ERR_CUDA;
   }
   auto kfn = attn_weights_kernel<kQStat, kN>;
   constexpr uint32_t smem = Shape<kQStat, kN>::kSmem;
