@@ -182,18 +182,22 @@ def _ref(dims: MLADims):
 def _here(dev: int, what: str, t, dtype, numel: int) -> int:
     """Address of a tensor that must be on the current device `dev`, contiguous, of `dtype` and
     at least `numel` elements."""
+    if (t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
+            and t.is_contiguous()):
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{what}: the tensor must live on the current CUDA device")
     if t.dtype is not dtype:
         raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    if t.numel() < numel or not t.is_contiguous():
-        raise ValueError(f"{what}: expected a contiguous tensor of at least {numel} elements")
-    return t.data_ptr()
+    raise ValueError(f"{what}: expected a contiguous tensor of at least {numel} elements")
 
 
 def _rows(dev: int, what: str, t, dtype, rows: int, width: int, stride: int) -> int:
     """Address of `rows` rows of `width` elements, `stride` apart, on the current device; the
     tensor is a view of them whose storage holds them all."""
+    if (t.dtype is dtype and t.get_device() == dev and stride >= width
+            and t.numel() >= rows * stride and t.is_contiguous()):
+        return t.data_ptr()
     if t.get_device() != dev:
         raise ValueError(f"{what}: the tensor must live on the current CUDA device")
     if t.dtype is not dtype:
@@ -424,18 +428,20 @@ def mla_norm_rope(dims: MLADims, y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batc
     dt, i32 = dims.torch_dtype, torch.int32
     H, dqk = dims.n_heads, dims.d_nope + dims.d_rope
     D = dims.d_latent + dims.d_rope
+    bi = sl = pt = pl = None
+    n_seqs = 0
+    if pool is not None:
+        n_seqs = page_table.numel() // max_pages if max_pages > 0 else 0
+        bi, sl = _here(dev, "batch_idx", batch_idx, i32, T), _here(dev, "slot", slot, i32, T)
+        pt = _here(dev, "page_table", page_table, i32, max_pages)
+        pl = _here(dev, "pool", pool, dt, n_pages * dims.page_size * D)
     _check("mla_norm_rope", lib().mla_norm_rope(
         _ref(dims), _rows(dev, "y", y, dt, T, H * dqk + D, y_stride_tok), y_stride_tok,
         None if w_q is None else _here(dev, "w_q", w_q, dt, dqk),
         None if w_c is None else _here(dev, "w_c", w_c, dt, dims.d_latent),
         None if w_kr is None else _here(dev, "w_kr", w_kr, dt, dims.d_rope), eps,
-        _here(dev, "pos", pos, i32, T),
-        None if pool is None else _here(dev, "batch_idx", batch_idx, i32, T),
-        None if pool is None else _here(dev, "slot", slot, i32, T),
-        None if pool is None else _here(dev, "page_table", page_table, i32, max_pages),
-        0 if pool is None else page_table.numel() // max_pages, max_pages,
-        None if pool is None else _here(dev, "pool", pool, dt, n_pages * dims.page_size * D),
-        n_pages, _rows(dev, "q", q, dt, T, H * dqk, q_stride_tok), q_stride_tok,
+        _here(dev, "pos", pos, i32, T), bi, sl, pt, n_seqs, max_pages, pl, n_pages,
+        _rows(dev, "q", q, dt, T, H * dqk, q_stride_tok), q_stride_tok,
         None if qbuf is None else _here(dev, "qbuf", qbuf, dt, T * H * D),
         None if ckr is None else _rows(dev, "ckr", ckr, dt, T, D, ckr_stride_tok), ckr_stride_tok,
         T, torch._C._cuda_getCurrentRawStream(dev)))

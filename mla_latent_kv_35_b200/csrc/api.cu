@@ -1038,11 +1038,14 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   a.max_tokens = max_pages * dims->page_size;
   a.n_sink = n_sink; a.n_recent = n_recent;
   // the fewest blocks whose threads hold a sequence's keys, and more while
-  // that leaves SMs idle and a block has more than 4096 slots
+  // that leaves SMs idle and a block has more than 8192 slots (a cluster
+  // barrier costs as much as a block's walk over some 4000)
+  constexpr long long kFew = (long long)kEvictFewKeys * kEvictThreads;
+  constexpr long long kMost = (long long)kEvictKeys * kEvictThreads;
   int cluster = 1;
   while (cluster < kEvictMaxCluster &&
-         (stride > (long long)kEvictSlots * cluster ||
-          (stride > 4096LL * cluster && 2LL * B * cluster <= sm_count())))
+         (stride > kMost * cluster ||
+          (stride > kFew * cluster && 2LL * B * cluster <= sm_count())))
     cluster *= 2;
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3((unsigned)(B * cluster));
@@ -1055,26 +1058,38 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  auto plan = stride <= (long long)kEvictSlots * cluster ? evict_plan_kernel<true>
-                                                         : evict_plan_kernel<false>;
+  auto plan = stride <= kFew * cluster    ? evict_plan_kernel<kEvictFewKeys>
+              : stride <= kMost * cluster ? evict_plan_kernel<kEvictKeys>
+                                          : evict_plan_kernel<0>;
   if (cudaLaunchKernelEx(&cfg, plan, a) != cudaSuccess) return MLA_ERR_CUDA;
   MLA_TRY(check_launch());
   const long long row_bytes = fp8_rows ? fp8::kRowBytes
                                        : (long long)(dims->d_latent + dims->d_rope) *
                                              (dims->dtype == MLA_F32 ? 4 : 2);
-  // at most eight blocks per SM, no more warps than pairs
-  const unsigned grid = (unsigned)std::min<long long>(
-      8LL * sm_count(), ((long long)B * stride / 2 + 7) / 8 + 1);
-  if (row_bytes % 16 == 0 && aligned16(pool))
-    evict_move_kernel<uint4><<<grid, 256, 0, st>>>(
-        static_cast<uint4*>(pool), (int)(row_bytes / 16), n_pages, dims->page_size, page_table,
-        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, B,
-        stride);
-  else
-    evict_move_kernel<uint16_t><<<grid, 256, 0, st>>>(
-        static_cast<uint16_t*>(pool), (int)(row_bytes / 2), n_pages, dims->page_size, page_table,
-        max_pages, weights, slot_pos, new_weights, new_pos, a.pairs, a.n_pairs, B,
-        stride);
+  // one wave (four blocks per SM), no more warps than there can be pairs; may
+  // start while the plan runs
+  cudaLaunchConfig_t mv{};
+  mv.gridDim = dim3((unsigned)std::min<long long>(4LL * sm_count(),
+                                                  ((long long)B * stride / 2 + 7) / 8 + 1));
+  mv.blockDim = dim3(256);
+  mv.stream = st;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  mv.attrs = at;
+  mv.numAttrs = 1;
+  const int2* pairs = a.pairs;
+  const int32_t* n_pairs = a.n_pairs;
+  const cudaError_t moved =
+      row_bytes % 16 == 0 && aligned16(pool)
+          ? cudaLaunchKernelEx(&mv, evict_move_kernel<uint4>, static_cast<uint4*>(pool),
+                               (int)(row_bytes / 16), n_pages, dims->page_size, page_table,
+                               max_pages, weights, slot_pos, new_weights, new_pos, pairs, n_pairs,
+                               B, (long long)stride)
+          : cudaLaunchKernelEx(&mv, evict_move_kernel<uint16_t>, static_cast<uint16_t*>(pool),
+                               (int)(row_bytes / 2), n_pages, dims->page_size, page_table,
+                               max_pages, weights, slot_pos, new_weights, new_pos, pairs, n_pairs,
+                               B, (long long)stride);
+  if (moved != cudaSuccess) return MLA_ERR_CUDA;
   return check_launch();
 }
 

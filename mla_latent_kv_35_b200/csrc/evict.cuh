@@ -20,8 +20,8 @@
 //     rank.  Nothing is sorted.  The first pass's sum is the number of free
 //     slots, so it needs no count of its own.
 //   * Every warp owns one run of consecutive slots, 32 at a time, and keeps
-//     their keys in registers (kCached: up to 16 per thread, 131072 slots in
-//     a cluster of 8; beyond that each pass reads the weights again).  Ranks
+//     their keys in registers (up to 16 per thread, 131072 slots in a
+//     cluster of 8; beyond that each pass reads the weights again).  Ranks
 //     within a run come from ballots; the runs' counts meet in one scan per
 //     block and one exchange per cluster.
 //   * Among equal keys the lowest slots leave.  Their ranks take another
@@ -44,8 +44,9 @@ namespace mla {
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictMaxCluster = 8;
 constexpr int kEvictBins = 2048;
-constexpr int kEvictKeys = 16;                              // keys a thread can hold
-constexpr int kEvictSlots = kEvictKeys * kEvictThreads;     // slots a block can hold
+// Keys a thread can hold: 8 where that is enough (fewer instructions per
+// thread: with 1024 threads the plan is bound by instruction issue), else 16.
+constexpr int kEvictFewKeys = 8, kEvictKeys = 16;
 constexpr int kEvictGroups = 2048;                          // sequence groups of the move
 
 struct EvictArgs {
@@ -138,8 +139,10 @@ __device__ __forceinline__ int2 evict_scan(EvictScan* sc, int2 count, int warp, 
   return before;
 }
 
-template <bool kCached>
+// kKeys: keys per thread; 0: every pass reads the weights again.
+template <int kKeys>
 __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictArgs a) {
+  constexpr bool kCached = kKeys > 0;
   __shared__ __align__(8) int hist[3][kEvictBins];   // one per pass: no barrier to reuse it
   __shared__ EvictScan scan_eq, scan_out;
   __shared__ int warp_sums[32];
@@ -147,6 +150,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   const uint32_t n = cluster_nctas(), rank = cluster_ctarank();
   const int b = blockIdx.x / n;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  pdl_launch();
   const int L = a.seq_lens[b];
   const bool bad = L < 0 || L > a.max_tokens || L > a.stride;
   const float* w = a.weights + b * a.stride;
@@ -160,7 +164,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
 
   // keys of this thread's slots s0 + 32 i + lane, and bit i of `free_bits`
   // where that slot is free
-  uint32_t key[kCached ? kEvictKeys : 1];
+  uint32_t key[kCached ? kKeys : 1];
   uint32_t free_bits = 0;
   int p1 = Lc - a.n_recent;              // free positions: [n_sink, p1)
   auto free_at = [&](int t) {
@@ -172,7 +176,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   auto each = [&](auto f) {
     if constexpr (kCached) {
 #pragma unroll
-      for (int i = 0; i < kEvictKeys; ++i)
+      for (int i = 0; i < kKeys; ++i)
         if (i < groups) f(i, key[i], (free_bits >> i & 1) != 0);
     } else {
       for (int i = 0; i < groups; ++i) {
@@ -191,20 +195,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     if constexpr (kCached) {
       // all loads first (a slot past the run reads the run's last one), so
       // that they are in flight together
-      int pos[kEvictKeys];
+      int pos[kKeys];
 #pragma unroll
-      for (int i = 0; i < kEvictKeys; ++i) {
+      for (int i = 0; i < kKeys; ++i) {
         key[i] = 0;
         if (i < groups) key[i] = __float_as_uint(w[min(s0 + 32 * i + lane, s1 - 1)]);
       }
 #pragma unroll
-      for (int i = 0; i < kEvictKeys; ++i) {
+      for (int i = 0; i < kKeys; ++i) {
         const int t = min(s0 + 32 * i + lane, s1 - 1);
         pos[i] = t;
         if (sp != nullptr && i < groups) pos[i] = sp[t];
       }
 #pragma unroll
-      for (int i = 0; i < kEvictKeys; ++i) {
+      for (int i = 0; i < kKeys; ++i) {
         const bool in = s0 + 32 * i + lane < s1;
         key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
         pos[i] = in ? pos[i] : -1;
@@ -221,7 +225,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
         p1 = mx + 1 - a.n_recent;
       }
 #pragma unroll
-      for (int i = 0; i < kEvictKeys; ++i)
+      for (int i = 0; i < kKeys; ++i)
         if (pos[i] >= max(a.n_sink, 0) && pos[i] < p1) free_bits |= 1u << i;
     } else {
       __syncthreads();
@@ -295,7 +299,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   // those of all slots with a bit in `stay`, four loads in flight
   auto keep_slots = [&](uint32_t stay) {
 #pragma unroll
-    for (int i0 = 0; i0 < kEvictKeys; i0 += 4) {
+    for (int i0 = 0; i0 < kKeys; i0 += 4) {
       if (i0 >= groups) break;
       float v[4];
       int p[4];
@@ -393,44 +397,67 @@ __global__ void __launch_bounds__(256) evict_move_kernel(
   __shared__ long long before[kEvictGroups + 1];   // pairs before each group of sequences
   __shared__ long long sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int per = (B + kEvictGroups - 1) / kEvictGroups, n_groups = (B + per - 1) / per;
-  long long base = 0;
-  for (int g0 = 0; g0 < n_groups; g0 += 256) {
-    const int g = g0 + threadIdx.x;
-    long long c = 0;
-    for (int b = g * per; g < n_groups && b < min(B, (g + 1) * per); ++b) c += n_pairs[b];
-    long long inc = c;
+  pdl_wait();
+  const long long warps = (long long)gridDim.x * 8, me = (long long)blockIdx.x * 8 + warp;
+  long long lo, hi;          // this warp's pairs
+  int b, i, n;               // sequence of pair lo, the pair within it, its pairs
+  if (B <= 32) {
+    // every warp scans for itself
+    const int mine = lane < B ? n_pairs[lane] : 0;
+    long long inc = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const long long y = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += y;
     }
-    if (lane == 31) sums[warp] = inc;
-    __syncthreads();
-    long long all = 0, front = 0;
-    for (int i = 0; i < 8; ++i) {
-      front += i < warp ? sums[i] : 0;
-      all += sums[i];
+    const long long all = __shfl_sync(0xffffffffu, inc, 31);
+    lo = all * me / warps;
+    hi = all * (me + 1) / warps;
+    if (lo >= hi) return;
+    b = __ffs(__ballot_sync(0xffffffffu, inc > lo)) - 1;
+    n = __shfl_sync(0xffffffffu, mine, b);
+    i = (int)(lo - (__shfl_sync(0xffffffffu, inc, b) - n));
+  } else {
+    const int per = (B + kEvictGroups - 1) / kEvictGroups, n_groups = (B + per - 1) / per;
+    long long base = 0;
+    for (int g0 = 0; g0 < n_groups; g0 += 256) {
+      const int g = g0 + threadIdx.x;
+      long long c = 0;
+      for (int s = g * per; g < n_groups && s < min(B, (g + 1) * per); ++s) c += n_pairs[s];
+      long long inc = c;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long y = __shfl_up_sync(0xffffffffu, inc, o);
+        if (lane >= o) inc += y;
+      }
+      if (lane == 31) sums[warp] = inc;
+      __syncthreads();
+      long long all = 0, front = 0;
+      for (int w = 0; w < 8; ++w) {
+        front += w < warp ? sums[w] : 0;
+        all += sums[w];
+      }
+      if (g < n_groups) before[g] = base + front + inc - c;
+      base += all;
+      __syncthreads();
     }
-    if (g < n_groups) before[g] = base + front + inc - c;
-    base += all;
+    if (threadIdx.x == 0) before[n_groups] = base;
     __syncthreads();
-  }
-  if (threadIdx.x == 0) before[n_groups] = base;
-  __syncthreads();
-  const long long warps = (long long)gridDim.x * 8, me = (long long)blockIdx.x * 8 + warp;
-  const long long lo = base * me / warps, hi = base * (me + 1) / warps;
-  if (lo >= hi) return;
-  // the sequence of pair lo
-  int ga = 0, gb = n_groups - 1;
-  while (ga < gb) {
-    const int mid = (ga + gb) >> 1;
-    if (before[mid + 1] > lo) gb = mid; else ga = mid + 1;
-  }
-  int b = ga * per, i = (int)(lo - before[ga]), n = n_pairs[b];
-  while (i >= n) {
-    i -= n;
-    n = n_pairs[++b];
+    lo = base * me / warps;
+    hi = base * (me + 1) / warps;
+    if (lo >= hi) return;
+    int ga = 0, gb = n_groups - 1;
+    while (ga < gb) {
+      const int mid = (ga + gb) >> 1;
+      if (before[mid + 1] > lo) gb = mid; else ga = mid + 1;
+    }
+    b = ga * per;
+    i = (int)(lo - before[ga]);
+    n = n_pairs[b];
+    while (i >= n) {
+      i -= n;
+      n = n_pairs[++b];
+    }
   }
   constexpr int kRows = 2;                 // rows in flight
   for (long long g = lo; g < hi;) {

@@ -104,7 +104,8 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   using namespace wtc;
   using S = Shape<kQStat, kN>;
   extern __shared__ uint8_t smem_raw[];
-  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages], stat_full, stat_empty;
+  __shared__ __align__(8) uint64_t full[kMaxStages], empty[kMaxStages];
+  __shared__ __align__(8) uint64_t stat_full[9], stat_empty[9];   // per 64-column chunk
   __shared__ __align__(8) uint64_t s_full[4], s_free[4], drain;
   __shared__ __align__(16) float lse2_sh[2][kN];
   __shared__ __align__(16) int lim_sh[2][kN];
@@ -124,8 +125,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       mbar_init(smem_u32(&full[s]), 1);      // the leader's arrive with both CTAs' bytes
       mbar_init(smem_u32(&empty[s]), 1);     // MMA commit (both CTAs)
     }
-    mbar_init(smem_u32(&stat_full), 1);
-    mbar_init(smem_u32(&stat_empty), 1);
+    for (int c = 0; c < 9; ++c) {
+      mbar_init(smem_u32(&stat_full[c]), 1);
+      mbar_init(smem_u32(&stat_empty[c]), 1);
+    }
     for (int b = 0; b < S::kBufs; ++b) {
       mbar_init(smem_u32(&s_full[b]), 1);    // MMA commit (both CTAs)
       mbar_init(smem_u32(&s_free[b]), 16);   // 8 epilogue warps x 2 CTAs
@@ -276,81 +279,103 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     return pg;
   };
 
+  // this CTA's pages of a tile: kCps chunks from chunk c on.  The leader arms a
+  // barrier with both CTAs' bytes; a page past the tile is not loaded (its
+  // rows compute on what the buffer held).
+  auto load_tile = [&](uint32_t dst, int c, int pg0, int pg1, uint32_t bar) {
+    if (pg0 >= 0) tma_load_5d_pair(dst, &tmK, 0, 0, c, 0, pg0, bar);
+    if (pg1 >= 0) tma_load_5d_pair(dst + S::kCps * 8192, &tmK, 0, 0, c, 0, pg1, bar);
+  };
+
   if (warp == 0 && lane == 0) {
-    // =====================  producer (both CTAs)  =====================
-    const uint32_t lead_full0 = mapa_shared(smem_u32(&full[0]), rank & ~1u);
-    const uint32_t lead_stat = mapa_shared(smem_u32(&stat_full), rank & ~1u);
-    uint32_t it = 0, stats = 0;
+    // ==============  producer of the ring (both CTAs)  ==============
+    const uint32_t lead_full0 = mapa_shared(smem_u32(&full[0]), 0);
+    uint32_t it = 0;
     bool ok = true;
-    int loaded = -1;                       // sequence whose rows are stationary
     // the next tile is looked up while this one loads: page ids take as long
     // as a box
     Walk next = w0;
     int npg0 = 0, npg1 = 0;
     bool more = walk_next(next);
-    if (more && next.blocks > 0) {
-      npg0 = page_at(next, 0);
-      npg1 = page_at(next, 1);
-    }
+    auto look = [&]() {
+      if (kQStat && more && next.blocks > 0) {
+        npg0 = page_at(next, 0);
+        npg1 = page_at(next, 1);
+      }
+    };
+    look();
     while (ok && more) {
       const Walk w = next;
       const int pg0 = npg0, pg1 = npg1;
       more = walk_next(next);
-      if (more && next.blocks > 0) {
-        npg0 = page_at(next, 0);
-        npg1 = page_at(next, 1);
-      }
-      if (w.blocks > 0) {
-        // the leader arms a barrier with both CTAs' bytes: a page past the
-        // tile is not loaded (its rows compute on what the stage held)
-        const uint32_t tile_bytes = (uint32_t)w.pages * S::kCps * 8192;
-        auto load_tile_chunk = [&](uint32_t dst, int c, uint32_t bar) {
-          if (pg0 >= 0) tma_load_5d_pair(dst, &tmK, 0, 0, c, 0, pg0, bar);
-          if (pg1 >= 0) tma_load_5d_pair(dst + S::kCps * 8192, &tmK, 0, 0, c, 0, pg1, bar);
-        };
-        if (!kQStat || loaded != w.b) {
-          // (the stationary operand is free once the MMAs on it completed)
-          if (stats > 0 && !mbar_wait(smem_u32(&stat_empty), (stats - 1) & 1, abort_p, 40, stats)) {
+      look();
+      const int steps = kQStat ? min(1, w.blocks) : w.blocks;
+      for (int rb = 0; rb < steps && ok; ++rb)
+        for (int c = 0; c < S::kSteps; ++c, ++it) {
+          const int s = it % S::kStages;
+          if (!mbar_wait(smem_u32(&empty[s]), ((it / S::kStages) & 1) ^ 1, abort_p, 41, it)) {
             ok = false;
             break;
           }
+          const uint32_t fb = lead_full0 + 8 * s;
           if (rank == 0)
-            mbar_expect_tx(smem_u32(&stat_full), kQStat ? 2 * S::kStat : 9 * tile_bytes);
-          for (int c = 0; c < 9; ++c) {
-            if constexpr (kQStat)
-              tma_load_2d_pair(sStat + c * (kN / 2) * 128, &tmQ, 64 * c,
-                               w.q0 * P.H + (kN / 2) * (int)rank, lead_stat);
-            else
-              load_tile_chunk(sStat + c * 16384, c, lead_stat);
-          }
-          ++stats;
-          loaded = w.b;
+            mbar_expect_tx(smem_u32(&full[s]),
+                           kQStat ? (uint32_t)w.pages * S::kCps * 8192 : 2 * S::kStage);
+          if constexpr (kQStat)
+            load_tile(sRing + s * S::kStage, S::kCps * c, pg0, pg1, fb);
+          else
+            tma_load_2d_pair(sRing + s * S::kStage, &tmQ, 64 * c,
+                             w.q0 * P.H + rb * kN + (kN / 2) * (int)rank, fb);
         }
-        const int steps = kQStat ? 1 : w.blocks;
-        for (int rb = 0; rb < steps && ok; ++rb)
-          for (int c = 0; c < S::kSteps; ++c, ++it) {
-            const int s = it % S::kStages;
-            if (!mbar_wait(smem_u32(&empty[s]), ((it / S::kStages) & 1) ^ 1, abort_p, 41, it)) {
-              ok = false;
-              break;
-            }
-            const uint32_t fb = lead_full0 + 8 * s;
-            if (rank == 0)
-              mbar_expect_tx(smem_u32(&full[s]), kQStat ? tile_bytes : 2 * S::kStage);
-            if constexpr (kQStat)
-              load_tile_chunk(sRing + s * S::kStage, S::kCps * c, fb);
-            else
-              tma_load_2d_pair(sRing + s * S::kStage, &tmQ, 64 * c,
-                               w.q0 * P.H + rb * kN + (kN / 2) * (int)rank, fb);
-          }
-      }
     }
-    if (!ok && rank == 0) {
+    if (!ok && rank == 0)
       // leaving early: wait (bounded) for the copies already armed
-      if (stats > 0) mbar_wait_bounded(smem_u32(&stat_full), (stats - 1) & 1, kDrainNs);
       for (uint32_t i = it > (uint32_t)S::kStages ? it - S::kStages : 0u; i < it; ++i)
         mbar_wait_bounded(smem_u32(&full[i % S::kStages]), (i / S::kStages) & 1, kDrainNs);
+  } else if (warp == 2 && lane == 0) {
+    // =====  producer of the resident operand (both CTAs), chunk by chunk  =====
+    // A chunk is reloaded once the last MMA on it completed, while the later
+    // chunks are still in use.
+    const uint32_t lead_stat0 = mapa_shared(smem_u32(&stat_full[0]), 0);
+    uint32_t stats = 0;
+    int armed = 0;                         // chunks of load `stats` under way
+    bool ok = true;
+    int loaded = -1;                       // sequence whose rows are resident
+    Walk w = w0;
+    while (ok && walk_next(w)) {
+      if (w.blocks == 0 || (kQStat && loaded == w.b)) continue;
+      int pg0 = 0, pg1 = 0;
+      if constexpr (!kQStat) {
+        pg0 = page_at(w, 0);
+        pg1 = page_at(w, 1);
+      }
+      for (int c = 0; c < 9; ++c) {
+        if (stats > 0 &&
+            !mbar_wait(smem_u32(&stat_empty[c]), (stats - 1) & 1, abort_p, 40, stats)) {
+          ok = false;
+          break;
+        }
+        const uint32_t fb = lead_stat0 + 8 * c;
+        if (rank == 0)
+          mbar_expect_tx(smem_u32(&stat_full[c]),
+                         kQStat ? 2 * (S::kStat / 9) : (uint32_t)w.pages * 8192);
+        if constexpr (kQStat)
+          tma_load_2d_pair(sStat + c * (S::kStat / 9), &tmQ, 64 * c,
+                           w.q0 * P.H + (kN / 2) * (int)rank, fb);
+        else
+          load_tile(sStat + c * 16384, c, pg0, pg1, fb);
+        ++armed;
+      }
+      if (ok) {
+        ++stats;
+        armed = 0;
+      }
+      loaded = w.b;
     }
+    if (rank == 0 && *abort_p)
+      for (int c = 0; c < 9; ++c)
+        if (c < armed || stats > 0)
+          mbar_wait_bounded(smem_u32(&stat_full[c]), (c < armed ? stats : stats - 1) & 1, kDrainNs);
   } else if (warp == 1 && lane == 0 && rank == 0) {
     // =====================  MMA issuer (leader)  =====================
     const uint32_t idesc = idesc_bf16_f32(256, kN, false, false);
@@ -362,47 +387,53 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     Walk w = w0;
     int loaded = -1;
     while (ok && walk_next(w)) {
-      const int b = w.b;
-      if (w.blocks > 0) {
-        if (!kQStat || loaded != b) {
-          ok = mbar_wait(smem_u32(&stat_full), stats & 1, abort_p, 42, stats);
-          ++stats;
-          loaded = b;
+      const int steps = kQStat ? min(1, w.blocks) : w.blocks;
+      for (int rb = 0; rb < steps && ok; ++rb, ++j) {
+        const bool fresh = kQStat ? loaded != w.b : rb == 0;       // just loaded
+        const bool done = kQStat ? w.last : rb == steps - 1;       // reloaded next
+        loaded = w.b;
+        const int buf = j % S::kBufs;
+        if (j >= (uint32_t)S::kBufs &&
+            !mbar_wait(smem_u32(&s_free[buf]), (j / S::kBufs - 1) & 1, abort_p, 43, j)) {
+          ok = false;
+          break;
         }
-        const int steps = kQStat ? 1 : w.blocks;
-        for (int rb = 0; rb < steps && ok; ++rb, ++j) {
-          const int buf = j % S::kBufs;
-          if (j >= (uint32_t)S::kBufs &&
-              !mbar_wait(smem_u32(&s_free[buf]), (j / S::kBufs - 1) & 1, abort_p, 43, j)) {
+        for (int k = 0; k < S::kSteps; ++k, ++it) {
+          const int s = it % S::kStages;
+          if (!mbar_wait(smem_u32(&full[s]), (it / S::kStages) & 1, abort_p, 44, it)) {
             ok = false;
             break;
           }
-          for (int k = 0; k < S::kSteps; ++k, ++it) {
-            const int s = it % S::kStages;
-            if (!mbar_wait(smem_u32(&full[s]), (it / S::kStages) & 1, abort_p, 44, it)) {
-              ok = false;
-              break;
-            }
+          auto issue = [&](int cc) {
+            const int c = k * S::kCps + cc;
+            const uint64_t st = stat_desc + (uint64_t)((c * (S::kStat / 9)) >> 4);
+            const uint64_t ri = ring_desc + (uint64_t)((s * S::kStage + cc * 1024) >> 4);
+#pragma unroll
+            for (int kk = 0; kk < 4; ++kk)
+              mma_bf16_ss<2>(tmem + kN * buf, (kQStat ? ri : st) + 2 * kk,
+                             (kQStat ? st : ri) + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+          };
+          if (!fresh && !done) {
             tc_fence_after();
 #pragma unroll
-            for (int cc = 0; cc < S::kCps; ++cc) {
+            for (int cc = 0; cc < S::kCps; ++cc)
+              if (k * S::kCps + cc < 9) issue(cc);
+          } else {
+            for (int cc = 0; cc < S::kCps && ok; ++cc) {
               const int c = k * S::kCps + cc;
               if (c >= 9) break;               // past the 576 columns
-              const uint64_t st = stat_desc + (uint64_t)((c * (S::kStat / 9)) >> 4);
-              const uint64_t ri = ring_desc + (uint64_t)((s * S::kStage + cc * 1024) >> 4);
-#pragma unroll
-              for (int kk = 0; kk < 4; ++kk)
-                mma_bf16_ss<2>(tmem + kN * buf, (kQStat ? ri : st) + 2 * kk,
-                               (kQStat ? st : ri) + 2 * kk, idesc, (c | kk) ? 1u : 0u);
+              ok = !fresh || mbar_wait(smem_u32(&stat_full[c]), stats & 1, abort_p, 42, stats);
+              if (!ok) break;
+              tc_fence_after();
+              issue(cc);
+              if (done) mma_commit_2_mc(smem_u32(&stat_empty[c]), 3);
             }
-            mma_commit_2_mc(smem_u32(&empty[s]), 3);
           }
-          if (ok) mma_commit_2_mc(smem_u32(&s_full[buf]), 3);
+          if (!ok) break;
+          mma_commit_2_mc(smem_u32(&empty[s]), 3);
         }
-      }
-      if (ok && loaded == b && (!kQStat || w.last)) {
-        mma_commit_2_mc(smem_u32(&stat_empty), 3);
-        loaded = -1;
+        if (ok) mma_commit_2_mc(smem_u32(&s_full[buf]), 3);
+        if (fresh) ++stats;
       }
     }
     if (!ok) {
@@ -427,7 +458,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       const int k = 2 * (int)rank + (tl >> 6);           // page of the tile
       const int t = (w.page + k) * kPage + (tl & 63);
       const int steps = kQStat ? min(1, w.blocks) : w.blocks;
-      float acc = 0.f;
+      const long long at = w.b * P.stride + t;
+      const bool store = ch == 0 && k < w.pages && t < w.L;
+      float acc = 0.f, old = 0.f;
+      if (store && P.w_in != nullptr && P.keep != 0.f && t < w.L - w.T) old = P.w_in[at];
       for (int rb = 0; rb < steps; ++rb, ++j) {
         // the rows' lse (in units of log2; +inf for a row that gives nothing)
         // and visible limits.  Two sets in turn: the barrier of the next
@@ -491,12 +525,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       if (ch == 1) red[done & 1][tl] = acc;
       leave = named_bar_or(2, kEpiThreads, dead || *abort_p != 0);
       if (leave) break;
-      if (ch == 0 && k < w.pages && t < w.L) {
-        const long long i = w.b * P.stride + t;
-        float v = acc + red[done & 1][tl];
-        if (P.w_in != nullptr && P.keep != 0.f && t < w.L - w.T) v = fmaf(P.keep, P.w_in[i], v);
-        P.w_out[i] = v;
-      }
+      if (store) P.w_out[at] = fmaf(P.keep, old, acc + red[done & 1][tl]);
       ++done;
     }
   }
