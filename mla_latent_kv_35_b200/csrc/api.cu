@@ -1037,14 +1037,14 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   a.stride = stride;
   a.max_tokens = max_pages * dims->page_size;
   a.n_sink = n_sink; a.n_recent = n_recent;
-  // the fewest blocks whose threads hold a sequence's keys, and more while
-  // that leaves SMs idle and a block has more than 8192 slots (a cluster
-  // barrier costs as much as a block's walk over some 4000)
+  // the fewest blocks whose threads hold all but a fifth of a sequence's keys,
+  // and more while that leaves SMs idle and a block has more than 8192 slots
+  // (a cluster barrier costs as much as a block's walk over some 4000)
   constexpr long long kFew = (long long)kEvictFewKeys * kEvictThreads;
   constexpr long long kMost = (long long)kEvictKeys * kEvictThreads;
   int cluster = 1;
   while (cluster < kEvictMaxCluster &&
-         (stride > kMost * cluster ||
+         (stride > kMost * cluster * 5 / 4 ||
           (stride > kFew * cluster && 2LL * B * cluster <= sm_count())))
     cluster *= 2;
   cudaLaunchConfig_t cfg{};
@@ -1058,9 +1058,8 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   at[0].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  auto plan = stride <= kFew * cluster    ? evict_plan_kernel<kEvictFewKeys>
-              : stride <= kMost * cluster ? evict_plan_kernel<kEvictKeys>
-                                          : evict_plan_kernel<0>;
+  auto plan = stride <= kFew * cluster ? evict_plan_kernel<kEvictFewKeys, false>
+                                       : evict_plan_kernel<kEvictKeys, true>;
   if (cudaLaunchKernelEx(&cfg, plan, a) != cudaSuccess) return MLA_ERR_CUDA;
   MLA_TRY(check_launch());
   const long long row_bytes = fp8_rows ? fp8::kRowBytes

@@ -20,8 +20,8 @@
 //     rank.  Nothing is sorted.  The first pass's sum is the number of free
 //     slots, so it needs no count of its own.
 //   * Every warp owns one run of consecutive slots, 32 at a time, and keeps
-//     their keys in registers (up to 16 per thread, 131072 slots in a
-//     cluster of 8; beyond that each pass reads the weights again).  Ranks
+//     their keys in registers (up to 16 per thread; each pass reads the
+//     weights of a longer run's rest again).  Ranks
 //     within a run come from ballots; the runs' counts meet in one scan per
 //     block and one exchange per cluster.
 //   * Among equal keys the lowest slots leave.  Their ranks take another
@@ -42,7 +42,7 @@
 namespace mla {
 
 constexpr int kEvictThreads = 1024;
-constexpr int kEvictMaxCluster = 8;
+constexpr int kEvictMaxCluster = 8;    // (16, beyond the portable size: 42 against 35 us)
 constexpr int kEvictBins = 2048;
 // Keys a thread can hold: 8 where that is enough (fewer instructions per
 // thread: with 1024 threads the plan is bound by instruction issue), else 16.
@@ -139,10 +139,9 @@ __device__ __forceinline__ int2 evict_scan(EvictScan* sc, int2 count, int warp, 
   return before;
 }
 
-// kKeys: keys per thread; 0: every pass reads the weights again.
-template <int kKeys>
+// kKeys: keys that a thread holds; kRest: a run may be longer than that.
+template <int kKeys, bool kRest>
 __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictArgs a) {
-  constexpr bool kCached = kKeys > 0;
   __shared__ __align__(8) int hist[3][kEvictBins];   // one per pass: no barrier to reuse it
   __shared__ EvictScan scan_eq, scan_out;
   __shared__ int warp_sums[32];
@@ -164,7 +163,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
 
   // keys of this thread's slots s0 + 32 i + lane, and bit i of `free_bits`
   // where that slot is free
-  uint32_t key[kCached ? kKeys : 1];
+  uint32_t key[kKeys];
   uint32_t free_bits = 0;
   int p1 = Lc - a.n_recent;              // free positions: [n_sink, p1)
   auto free_at = [&](int t) {
@@ -174,15 +173,12 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   // f(i, key, free) over this thread's groups; key and free of a slot past the
   // run are 0 and false
   auto each = [&](auto f) {
-    if constexpr (kCached) {
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (i < groups) f(i, key[i], (free_bits >> i & 1) != 0);
-    } else {
-      for (int i = 0; i < groups; ++i) {
-        const int t = s0 + 32 * i + lane;
-        f(i, t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t));
-      }
+    for (int i = 0; i < kKeys; ++i)
+      if (i < groups) f(i, key[i], (free_bits >> i & 1) != 0);
+    for (int i = kKeys; kRest && i < groups; ++i) {
+      const int t = s0 + 32 * i + lane;
+      f(i, t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t));
     }
   };
 
@@ -192,54 +188,42 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     for (int i = threadIdx.x; i < 3 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
     if (threadIdx.x == 0) max_sh = -1;
     int mx = -1;
-    if constexpr (kCached) {
-      // all loads first (a slot past the run reads the run's last one), so
-      // that they are in flight together
-      int pos[kKeys];
+    // all loads first (a slot past the run reads the run's last one), so that
+    // they are in flight together
+    int pos[kKeys];
 #pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        key[i] = 0;
-        if (i < groups) key[i] = __float_as_uint(w[min(s0 + 32 * i + lane, s1 - 1)]);
-      }
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        const int t = min(s0 + 32 * i + lane, s1 - 1);
-        pos[i] = t;
-        if (sp != nullptr && i < groups) pos[i] = sp[t];
-      }
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        const bool in = s0 + 32 * i + lane < s1;
-        key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
-        pos[i] = in ? pos[i] : -1;
-        mx = max(mx, pos[i]);
-      }
-      __syncthreads();
-      if (sp != nullptr) {
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        if (lane == 0) atomicMax(&max_sh, mx);
-        if (n > 1) cluster_sync(); else __syncthreads();
-        mx = max_sh;
-        if (n > 1)
-          for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
-        p1 = mx + 1 - a.n_recent;
-      }
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i)
-        if (pos[i] >= max(a.n_sink, 0) && pos[i] < p1) free_bits |= 1u << i;
-    } else {
-      __syncthreads();
-      if (sp != nullptr) {
-        for (int t = s0 + lane; t < s1; t += 32) mx = max(mx, sp[t]);
-        mx = __reduce_max_sync(0xffffffffu, mx);
-        if (lane == 0) atomicMax(&max_sh, mx);
-        if (n > 1) cluster_sync(); else __syncthreads();
-        mx = max_sh;
-        if (n > 1)
-          for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
-        p1 = mx + 1 - a.n_recent;
-      }
+    for (int i = 0; i < kKeys; ++i) {
+      key[i] = 0;
+      if (i < groups) key[i] = __float_as_uint(w[min(s0 + 32 * i + lane, s1 - 1)]);
     }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const int t = min(s0 + 32 * i + lane, s1 - 1);
+      pos[i] = t;
+      if (sp != nullptr && i < groups) pos[i] = sp[t];
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i) {
+      const bool in = s0 + 32 * i + lane < s1;
+      key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
+      pos[i] = in ? pos[i] : -1;
+      mx = max(mx, pos[i]);
+    }
+    if (kRest && sp != nullptr)
+      for (int t = s0 + 32 * kKeys + lane; t < s1; t += 32) mx = max(mx, sp[t]);
+    __syncthreads();
+    if (sp != nullptr) {
+      mx = __reduce_max_sync(0xffffffffu, mx);
+      if (lane == 0) atomicMax(&max_sh, mx);
+      if (n > 1) cluster_sync(); else __syncthreads();
+      mx = max_sh;
+      if (n > 1)
+        for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
+      p1 = mx + 1 - a.n_recent;
+    }
+#pragma unroll
+    for (int i = 0; i < kKeys; ++i)
+      if (pos[i] >= a.n_sink && pos[i] < p1) free_bits |= 1u << i;
 
     // ---- the n_out-th smallest key, digit by digit ----
 #pragma unroll
@@ -340,18 +324,20 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
       eq += __popc(e);
       return __ballot_sync(0xffffffffu, fr && (k < kth || (k == kth && r < need)));
     };
-    // slots of group i before slot `end`, as a mask of lanes
-    auto until = [&](int i, int end) {
-      const int d = end - (s0 + 32 * i);
-      return d >= 32 ? 0xffffffffu : d > 0 ? (1u << d) - 1 : 0u;
-    };
+    // slots of group i before the new end, and slots of the run, as masks of
+    // lanes
+    const int gf = max(new_len - s0, 0) / 32;
+    const uint32_t edge = new_len > s0 ? (1u << ((new_len - s0) & 31)) - 1 : 0u;
+    const uint32_t tail = s1 - s0 == 32 * groups ? 0xffffffffu : (1u << ((s1 - s0) & 31)) - 1;
+    auto front_of = [&](int i) { return i < gf ? 0xffffffffu : i == gf ? edge : 0u; };
+    auto run_of = [&](int i) { return i == groups - 1 ? tail : 0xffffffffu; };
     // ---- ranks of the vacated and the moving slots ----
     int eq = eq0;
     int2 c = make_int2(0, 0);
     each([&](int i, uint32_t k, bool fr) {
-      const uint32_t out = leaving(k, fr, eq), front = until(i, new_len);
+      const uint32_t out = leaving(k, fr, eq), front = front_of(i);
       c.x += __popc(out & front);
-      c.y += __popc(until(i, s1) & ~out & ~front);
+      c.y += __popc(run_of(i) & ~out & ~front);
     });
     int2 sum, at = evict_scan(&scan_out, c, warp, lane, rank, n, &sum);
     n_hole = sum.x;
@@ -360,19 +346,19 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     uint32_t stay = 0;          // bit i: slot i of this thread stays where it is
     each([&](int i, uint32_t k, bool fr) {
       const int t = s0 + 32 * i + lane;
-      const uint32_t out = leaving(k, fr, eq), front = until(i, new_len);
-      const uint32_t h = out & front, m = until(i, s1) & ~out & ~front;
+      const uint32_t out = leaving(k, fr, eq), front = front_of(i);
+      const uint32_t h = out & front, m = run_of(i) & ~out & ~front;
       if (h >> lane & 1) pairs[at.x + __popc(h & lower)].x = t;
       if (m >> lane & 1) pairs[at.y + __popc(m & lower)].y = t;
       at.x += __popc(h);
       at.y += __popc(m);
-      const bool stays = (until(i, s1) & front & ~out) >> lane & 1;
-      if constexpr (kCached)
+      const bool stays = (run_of(i) & front & ~out) >> lane & 1;
+      if (i < kKeys)
         stay |= (uint32_t)stays << i;
       else if (stays)
         keep_slot(t);
     });
-    if constexpr (kCached) keep_slots(stay);
+    keep_slots(stay);
   } else {
     for (int t = s0 + lane; t < s1; t += 32) keep_slot(t);
   }
