@@ -9,6 +9,11 @@
   A4+A5 mla_decode      split-KV attention on the latent cache + LSE combine
   A6  mla_out_proj      W_UV per head, then W_O
 
+``MLADecodeLayer.extend`` is the same step for ragged chunks of new tokens
+(mla_chunk_attention); ``gather_weights`` and ``evict`` keep a cache within a
+budget by the attention its tokens receive.  A layer whose weights hold norms
+(N_Q, N_C, N_KR) runs mla_norm_rope in place of A2 and A3.
+
 Torch only provides device memory and the stream; every step runs in the
 library's kernels.
 """
@@ -29,7 +34,10 @@ def _to_dev(x: np.ndarray, dtype, device):
 class MLADecodeLayer:
     """Weights and cache of one MLA layer on one GPU."""
 
-    def __init__(self, dims: MLADims, weights: dict, device="cuda"):
+    def __init__(self, dims: MLADims, weights: dict, device="cuda", norm_eps: float = 1e-6):
+        """weights: W_Q, W_DKV, W_KR, W_UK, W_UV, W_O, and any of the RMS norms
+        N_Q [d_nope + d_rope] (every query head), N_C [d_latent] (the latent)
+        and N_KR [d_rope] (the RoPE key, before its rotation)."""
         self.dims = dims
         self.device = torch.device(device)
         dt = dims.torch_dtype
@@ -42,6 +50,10 @@ class MLADecodeLayer:
         self.W_UK = _to_dev(weights["W_UK"], dt, self.device)
         self.W_UV = _to_dev(weights["W_UV"], dt, self.device)
         self.W_O = _to_dev(weights["W_O"], dt, self.device)
+        self.norms = [_to_dev(weights[k], dt, self.device) if weights.get(k) is not None else None
+                      for k in ("N_Q", "N_C", "N_KR")]
+        self.normed = any(n is not None for n in self.norms)
+        self.norm_eps = norm_eps
         self._bufs = {}
         self.pool = None
         self.cache_kind = "bf16"
@@ -70,7 +82,8 @@ class MLADecodeLayer:
 
     def prefill_from_hidden(self, h_ctx_list):
         """Fill each sequence's prior tokens from hidden states: project with
-        [W_DKV; W_KR], rotate the RoPE keys at positions 0.., append."""
+        [W_DKV; W_KR] (and norm), rotate the RoPE keys at positions 0..,
+        append."""
         d = self.dims
         H = d.n_heads
         w_ckv = self.W_A0[H * self.dqk:]
@@ -79,6 +92,13 @@ class MLADecodeLayer:
             if n == 0:
                 continue
             hd = _to_dev(h, d.torch_dtype, self.device)
+            if self.normed:
+                y = torch.empty((n, self.Y), dtype=d.torch_dtype, device=self.device)
+                _b.mla_project(d, hd, self.W_A0, y, n, d.d_model, self.Y)
+                pos = torch.arange(n, dtype=torch.int32, device=self.device)
+                bi = torch.full((n,), b, dtype=torch.int32, device=self.device)
+                self._norm_rope_append(y, None, bi, pos, pos, n)
+                continue
             y = torch.empty((n, self.D), dtype=d.torch_dtype, device=self.device)
             _b.mla_project(d, hd, w_ckv, y, n, d.d_model, self.D)
             pos = torch.arange(n, dtype=torch.int32, device=self.device)
@@ -117,25 +137,31 @@ class MLADecodeLayer:
     # ------------------------------------------------------------------
     # the hot path
     # ------------------------------------------------------------------
-    def step(self, h, batch_idx, pos, B: int, S_q: int, num_workers: int = 0,
-             fused: bool = True, slot: int = 0):
-        """h [T, d_model] device (dims dtype), batch_idx/pos int32 [T] device,
-        T = B*S_q tokens b-major.  Returns the dict of step buffers.
-
-        fused: A1-A3 through mla_pre_attention (one launch for bf16) instead
-        of the four separate calls; both write the same bits.  An 8-bit
-        cache always takes the separate calls, its append quantizing the new
-        rows (mla_cache_append_fp8)."""
+    def _norm_rope_append(self, y, qbuf, batch_idx, pos, places, T: int):
+        """Norms, rotation and append of T rows of A0 output, in place."""
         d = self.dims
-        H, dn, dc, dr = d.n_heads, d.d_nope, d.d_latent, d.d_rope
-        T = B * S_q
-        bf = self.buffers(B, S_q, num_workers, slot)
+        fp8 = self.cache_kind == "fp8"
+        ckr = y[:, d.n_heads * self.dqk:]
+        _b.mla_norm_rope(d, y, self.Y, *self.norms, self.norm_eps, pos, batch_idx, places,
+                         self.page_table, self.max_pages, None if fp8 else self.pool,
+                         self.n_pages, y, self.Y, qbuf, ckr if fp8 else None,
+                         self.Y if fp8 else 0, T)
+        if fp8:
+            _b.mla_cache_append_fp8(d, ckr, self.Y, ckr[:, d.d_latent:], self.Y, batch_idx, places,
+                                    self.page_table, self.max_pages, self.pool, self.n_pages, T)
+
+    def _pre_attention(self, bf, batch_idx, pos, places, T: int, fused: bool):
+        """A1-A3 on the A0 rows bf["y"]: qbuf filled, the new rows cached."""
+        d = self.dims
+        H, dn, dc = d.n_heads, d.d_nope, d.d_latent
         y, qbuf = bf["y"], bf["qbuf"]
         Y, D, dqk = self.Y, self.D, self.dqk
-        _b.mla_project(d, h, self.W_A0, y, T, d.d_model, Y)                        # A0
         fp8 = self.cache_kind == "fp8"
-        if fused and not fp8:
-            _b.mla_pre_attention(d, y, Y, self.W_UK, qbuf, batch_idx, pos,          # A1-A3
+        if self.normed:
+            self._norm_rope_append(y, qbuf, batch_idx, pos, pos if places is None else places, T)
+            _b.mla_absorb_q(d, y, Y, self.W_UK, qbuf, T)
+        elif fused and not fp8 and places is None:
+            _b.mla_pre_attention(d, y, Y, self.W_UK, qbuf, batch_idx, pos,
                                  self.page_table, self.max_pages, self.pool, self.n_pages, T)
         else:
             off_c = H * dqk
@@ -143,9 +169,31 @@ class MLADecodeLayer:
             kr = y[:, off_c + dc:]
             _b.mla_rope(d, kr, Y, 0, 1, kr, Y, 0, pos, T)                             # A2 k
             append = _b.mla_cache_append_fp8 if fp8 else _b.mla_cache_append
-            append(d, y[:, off_c:], Y, kr, Y, batch_idx, pos,                         # A3
+            append(d, y[:, off_c:], Y, kr, Y, batch_idx, pos if places is None else places,  # A3
                    self.page_table, self.max_pages, self.pool, self.n_pages, T)
             _b.mla_absorb_q(d, y, Y, self.W_UK, qbuf, T)                               # A1
+
+    def step(self, h, batch_idx, pos, B: int, S_q: int, num_workers: int = 0,
+             fused: bool = True, slot: int = 0, places=None):
+        """h [T, d_model] device (dims dtype), batch_idx/pos int32 [T] device,
+        T = B*S_q tokens b-major.  Returns the dict of step buffers.
+
+        fused: A1-A3 through mla_pre_attention (one launch for bf16) instead
+        of the four separate calls; both write the same bits.  An 8-bit
+        cache always takes the separate calls, its append quantizing the new
+        rows (mla_cache_append_fp8).  A layer with norms takes mla_norm_rope
+        and the absorb GEMM.
+
+        places: int32 [T] device, the tokens' slots in their sequences' pages
+        where they differ from pos (after evict); the last S_q slots below
+        seq_lens."""
+        d = self.dims
+        T = B * S_q
+        bf = self.buffers(B, S_q, num_workers, slot)
+        qbuf = bf["qbuf"]
+        _b.mla_project(d, h, self.W_A0, bf["y"], T, d.d_model, self.Y)             # A0
+        fp8 = self.cache_kind == "fp8"
+        self._pre_attention(bf, batch_idx, pos, places, T, fused)                    # A1-A3
         decode = _b.mla_decode_fp8 if fp8 else _b.mla_decode
         decode(d, qbuf, self.pool, self.n_pages, self.page_table,                     # A4+A5
                self.max_pages, self.seq_lens, B, S_q, num_workers, bf["ws"],
@@ -153,6 +201,89 @@ class MLADecodeLayer:
         _b.mla_out_proj(d, bf["o_lat"], self.W_UV, self.W_O, bf["scratch"],         # A6
                         bf["out"], T)
         return bf
+
+    # ------------------------------------------------------------------
+    # ragged chunks, gathered weights, eviction
+    # ------------------------------------------------------------------
+    def _absorbed_only(self, what: str):
+        if self.dims.dtype != "bf16" or self.cache_kind != "bf16":
+            raise ValueError(f"{what} needs a bf16 layer and a bf16 cache")
+
+    def extend_buffers(self, B: int, T: int, max_q: int):
+        """Device buffers of one extend() of B sequences and T tokens."""
+        key = ("extend", B, T, max_q)
+        if key not in self._bufs:
+            d = self.dims
+            dev, dt, H = self.device, d.torch_dtype, d.n_heads
+            self._bufs[key] = dict(
+                y=torch.empty((T, self.Y), dtype=dt, device=dev),
+                qbuf=torch.empty((T, H, self.D), dtype=dt, device=dev),
+                o_lat=torch.empty((T, H, d.d_latent), dtype=dt, device=dev),
+                lse=torch.empty((T, H), dtype=torch.float32, device=dev),
+                out=torch.empty((T, d.d_model), dtype=torch.float32, device=dev),
+                ws=torch.empty((_b.mla_chunk_attention_workspace_size(d, B, T, max_q),),
+                               dtype=torch.uint8, device=dev),
+                scratch=torch.empty((_b.mla_out_proj_bf16_scratch_size(d, T),),
+                                    dtype=torch.uint8, device=dev))
+        return self._bufs[key]
+
+    def extend(self, h, batch_idx, pos, cu_q, T: int, max_q: int, fused: bool = True,
+               places=None):
+        """One step of ragged chunks: sequence b brings the tokens cu_q[b] ..
+        cu_q[b+1]-1 of h [T, d_model] (device, dims dtype), the last of its
+        seq_lens[b] cached tokens.
+
+        cu_q int32 [B+1] device, batch_idx and pos int32 [T] device, max_q >=
+        the longest chunk; places as for step().  Decode tokens, speculative
+        tokens and prompt tails go through one call:
+
+          A0  mla_project, A1-A3 as in step(), mla_chunk_attention,
+          mla_out_proj_bf16
+
+        Returns the dict of buffers (out fp32 [T, d_model], o_lat bf16, lse,
+        qbuf).  bf16 layers with a bf16 cache."""
+        self._absorbed_only("extend")
+        d = self.dims
+        B = self.page_table.shape[0]
+        bf = self.extend_buffers(B, T, max_q)
+        _b.mla_project(d, h, self.W_A0, bf["y"], T, d.d_model, self.Y)
+        self._pre_attention(bf, batch_idx, pos, places, T, fused)
+        _b.mla_chunk_attention(d, bf["qbuf"], cu_q, T, max_q, self.pool, self.n_pages,
+                               self.page_table, self.max_pages, self.seq_lens, B, bf["ws"],
+                               bf["o_lat"], bf["lse"])
+        _b.mla_out_proj_bf16(d, bf["o_lat"], self.W_UV, self.W_O, bf["scratch"], bf["out"], T)
+        return bf
+
+    def gather_weights(self, bf, cu_q, T: int, max_q: int, weights, keep: float = 1.0):
+        """Add to weights (fp32 [B, tokens] device, in place) the attention
+        weight that every cached token received from the queries of the step
+        or extend() that returned bf, what was there before times keep.  The
+        step's own tokens start from nothing.  For a step, cu_q is 0, S_q,
+        2 S_q, .. and T = B*S_q."""
+        self._absorbed_only("gather_weights")
+        _b.mla_attn_weights(self.dims, bf["qbuf"], bf["lse"], cu_q, T, max_q, self.pool,
+                            self.n_pages, self.page_table, self.max_pages, self.seq_lens,
+                            self.page_table.shape[0], weights, keep, weights, weights.shape[1])
+
+    def evict(self, weights, budget, n_sink: int = 0, n_recent: int = 0, slot_pos=None):
+        """Cut every sequence to budget[b] tokens (int32 [B] device): those with
+        the least gathered weight leave, the first n_sink and the last
+        n_recent positions excepted, and the survivors behind the new end move
+        into their slots.  Updates pool, seq_lens, weights and slot_pos (int32
+        [B, tokens], the position of every slot's token; None while slots
+        follow positions) in place.  Any layer and cache kind.
+
+        New tokens then go to the slots from seq_lens on (places of step() and
+        extend()) at their own positions."""
+        d = self.dims
+        B, width = weights.shape
+        key = ("evict", B, width)
+        if key not in self._bufs:
+            self._bufs[key] = torch.empty((_b.mla_cache_evict_workspace_size(d, B, width),),
+                                          dtype=torch.uint8, device=self.device)
+        _b.mla_cache_evict(d, self.pool, self.n_pages, self.cache_kind == "fp8", self.page_table,
+                           self.max_pages, self.seq_lens, B, weights, slot_pos, width, budget,
+                           n_sink, n_recent, weights, slot_pos, self.seq_lens, self._bufs[key])
 
     # ------------------------------------------------------------------
     # chunked prefill (non-absorbed)
@@ -189,6 +320,7 @@ class MLADecodeLayer:
           P0  mla_project            y = [W_Q; W_DKV; W_KR] h
           P0  mla_rope (x2)          q_rope and k_rope rotated in place in y
           P0  mla_cache_append       [c ; k_rope] -> paged pool
+              (a layer with norms: mla_norm_rope for these three)
           P1  mla_prefill_rebuild_kv ctx rows, k_nope, v of the L tokens
           P2  mla_prefill_attention  o [T, H, d_v], lse [T, H]
           P3  mla_project            out = W_O o  (bf16 [T, d_model])
@@ -205,11 +337,14 @@ class MLADecodeLayer:
         bf = self.prefill_buffers(T, L, slot)
         y = bf["y"]
         _b.mla_project(d, h, self.W_A0, y, T, d.d_model, Y)
-        _b.mla_rope(d, y[:, dn:], Y, dqk, H, y[:, dn:], Y, dqk, pos, T)
-        kr = y[:, off_c + dc:]
-        _b.mla_rope(d, kr, Y, 0, 1, kr, Y, 0, pos, T)
-        _b.mla_cache_append(d, y[:, off_c:], Y, kr, Y, batch_idx, pos, self.page_table,
-                            self.max_pages, self.pool, self.n_pages, T)
+        if self.normed:
+            self._norm_rope_append(y, None, batch_idx, pos, pos, T)
+        else:
+            _b.mla_rope(d, y[:, dn:], Y, dqk, H, y[:, dn:], Y, dqk, pos, T)
+            kr = y[:, off_c + dc:]
+            _b.mla_rope(d, kr, Y, 0, 1, kr, Y, 0, pos, T)
+            _b.mla_cache_append(d, y[:, off_c:], Y, kr, Y, batch_idx, pos, self.page_table,
+                                self.max_pages, self.pool, self.n_pages, T)
         _b.mla_prefill_rebuild_kv(d, self.pool, self.n_pages, self.page_table[b], L, self.W_UK,
                                   self.W_UV, bf["ctx"], bf["k_nope"], bf["v"])
         _b.mla_prefill_attention(d, y, Y, bf["ctx"], bf["k_nope"], bf["v"], T, L, bf["o"],
