@@ -70,8 +70,8 @@ __device__ __forceinline__ bool chunk_bad(const int32_t* cu_q, int b, int total_
 // of their token blocks.  A cu_q that breaks its rules anywhere gives no
 // blocks at all: chunks could overlap.  A sequence whose length is impossible
 // keeps its rows with nothing to see (one empty block), so that they come out
-// as 0 and -inf.  first: [B + 1], scratch for B > kPlanSeqs.  cuts[k], k <
-// G - 1: the virtual sequence that the boundary between workers k and k + 1
+// as 0 and -inf.  first: [B + 1], scratch for B > kPlanSeqs.  worker_v[k]: the
+// virtual sequence of worker k's first block.  cuts[k], k < G - 1: the virtual sequence that the boundary between workers k and k + 1
 // cuts (-1: none), with its first and last worker.
 constexpr int kPlanSeqs = 2048;
 struct ChunkCut {
@@ -82,7 +82,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
                                                           int total_q, int max_q, int max_tokens,
                                                           int V, int G, int32_t* first_global,
                                                           VSeq* vseq, int32_t* start,
-                                                          ChunkCut* cuts) {
+                                                          ChunkCut* cuts, int32_t* worker_v) {
   __shared__ int warp_sums[32];
   __shared__ int first_sh[kPlanSeqs + 1];
   pdl_launch();
@@ -142,6 +142,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
     if (v1 <= v0) continue;
     const int k0 = worker_of(v0, blocks, workers), k1 = worker_of(v1 - 1, blocks, workers);
     for (int k = k0; k < k1; ++k) cuts[k] = ChunkCut{v, k0, k1, 0};
+    for (int k = worker_lo(k0, blocks, workers) < v0 ? k0 + 1 : k0; k <= k1; ++k) worker_v[k] = v;
   }
 }
 
@@ -223,7 +224,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse,
 struct ChunkLayout {
   long long V;
   int G;
-  size_t off_first, off_vseq, off_cuts, off_lse, off_o, total;
+  size_t off_first, off_vseq, off_cuts, off_wv, off_lse, off_o, total;
 };
 
 inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
@@ -234,7 +235,8 @@ inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
   c.off_first = up(sizeof(int32_t) * (c.V + 1));
   c.off_vseq = c.off_first + up(sizeof(int32_t) * ((size_t)B + 1));
   c.off_cuts = c.off_vseq + up(sizeof(VSeq) * c.V);
-  c.off_lse = c.off_cuts + up(sizeof(ChunkCut) * G);
+  c.off_wv = c.off_cuts + up(sizeof(ChunkCut) * G);
+  c.off_lse = c.off_wv + up(sizeof(int32_t) * G);
   c.off_o = c.off_lse + up(sizeof(float) * 2 * G * 128);
   c.total = c.off_o + sizeof(float) * 2 * G * 128 * dtc::kDC;
   return c;
@@ -251,6 +253,7 @@ inline mla_status launch_chunk_tc_impl(
   int32_t* first = reinterpret_cast<int32_t*>(ws + c.off_first);
   VSeq* vseq = reinterpret_cast<VSeq*>(ws + c.off_vseq);
   ChunkCut* cuts = reinterpret_cast<ChunkCut*>(ws + c.off_cuts);
+  int32_t* worker_v = reinterpret_cast<int32_t*>(ws + c.off_wv);
   float* ws_lse = reinterpret_cast<float*>(ws + c.off_lse);
   float* ws_o = reinterpret_cast<float*>(ws + c.off_o);
   CUtensorMap tQ, tQK, tPV;
@@ -260,7 +263,8 @@ inline mla_status launch_chunk_tc_impl(
                            (int)kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
   chunk_plan_kernel<<<1, 1024, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
-                                        (int)c.V, c.G, first, vseq, start, cuts);
+                                        (int)c.V, c.G, first, vseq, start, cuts,
+                                        worker_v);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   DecodeTcParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
@@ -276,6 +280,7 @@ inline mla_status launch_chunk_tc_impl(
   p.G = c.G;
   p.scale_log2 = scale * 1.4426950408889634f;
   p.vseq = vseq;
+  p.worker_v = worker_v;
   p.V = (int)c.V;
   p.o = o;
   p.lse = lse;

@@ -150,6 +150,7 @@ struct DecodeTcParams {
   float scale_log2;       // softmax scale * log2(e)
   // ragged chunks only
   const VSeq* vseq;       // [V]
+  const int32_t* worker_v;   // [G] virtual sequence of each worker's first block
   int V;
   __nv_bfloat16* o;       // [total_q][H][512]
   float* lse;             // [total_q][H]
@@ -176,6 +177,39 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
   return r != 0;
 }
 
+// Stores a warp's 32 x 32 words (lane = row) as rows of 128 contiguous bytes,
+// `pitch` bytes apart, of which the first `valid` exist.  Eight rows at a time
+// turn around in the warp's 1 KB of shared memory, so that a store instruction
+// covers four whole lines instead of sixteen bytes of 32 (O of a piece: 6.4 ->
+// 1.5 us).
+__device__ __forceinline__ void store_rows32(uint32_t sx, const uint32_t (&x)[32], uint8_t* dst,
+                                             size_t pitch, int valid, int lane) {
+  const int r = lane & 7;
+#pragma unroll
+  for (int g = 0; g < 4; ++g) {
+    if ((lane >> 3) == g) {
+#pragma unroll
+      for (int u = 0; u < 8; ++u)
+        asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(sx + r * 128 + ((u ^ r) << 4)),
+                     "r"(x[4 * u]), "r"(x[4 * u + 1]), "r"(x[4 * u + 2]), "r"(x[4 * u + 3])
+                     : "memory");
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const int q = (lane >> 3) + 4 * k;
+      uint4 v;
+      asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                   : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                   : "r"(sx + q * 128 + ((r ^ q) << 4))
+                   : "memory");
+      if (8 * g + q < valid)
+        *reinterpret_cast<uint4*>(dst + (size_t)(8 * g + q) * pitch + r * 16) = v;
+    }
+    __syncwarp();
+  }
+}
+
 __device__ __forceinline__ void named_bar_sync(int id, int nthreads) {
   asm volatile("barrier.sync %0, %1;" ::"r"(id), "r"(nthreads) : "memory");
 }
@@ -194,6 +228,11 @@ struct PieceIter {
   __device__ void init(const int32_t* s, int V_, int lo_, int hi_) {
     start = s; V = V_; lo = lo_; hi = hi_;
     v = (lo < hi) ? seq_of_block(start, V, lo) : V;
+  }
+  // v_: the virtual sequence of block lo, where the planner has listed it
+  __device__ void init(const int32_t* s, int V_, int lo_, int hi_, int v_) {
+    start = s; V = V_; lo = lo_; hi = hi_;
+    v = (lo < hi) ? v_ : V;
   }
   // next piece with at least one block; returns false when done
   __device__ bool next(int& pv, int& x0, int& x1) {
@@ -307,6 +346,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
   const int lo = total > 0 && worker < G ? worker_lo(worker, total, G) : 0;
   const int hi = total > 0 && worker < G ? worker_lo(worker + 1, total, G) : 0;
 
+  // (a search over the prefix sums takes a trip to L2 per step)
+  auto pieces = [&](PieceIter& it) {
+    if constexpr (kRagged)
+      it.init(P.start, V, lo, hi, P.worker_v[worker]);
+    else
+      it.init(P.start, V, lo, hi);
+  };
+
   // Registers: the control warpgroup (producers, MMA) gives up most
   // of its share to the two softmax warpgroups.
   static_assert(128 * kRegsControl + 256 * kRegsSoftmax <= kRegsLaunch * kThreads &&
@@ -321,7 +368,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       const uint32_t lead_qfull = mapa_shared(smem_u32(&q_full), 0);
       uint32_t it = 0, q_issued = 0;
       PieceIter pi;
-      pi.init(P.start, V, lo, hi);
+      pieces(pi);
       int v, x0, x1, piece = 0;
       bool ok = true;
       while (ok && pi.next(v, x0, x1)) {
@@ -395,7 +442,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       const uint32_t lead_full0 = mapa_shared(smem_u32(&pv_full[0]), 0);
       uint32_t it = 0;
       PieceIter pi;
-      pi.init(P.start, V, lo, hi);
+      pieces(pi);
       int v, x0, x1;
       bool ok = true;
       const int rsub = lane >> 4, cc = (lane >> 3) & 1, u = lane & 7;
@@ -465,7 +512,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       // the 16 slot groups of a chunk (both pages) lie 1 KB x kQkCps apart
       const uint64_t qk_desc = sw128_desc(sQk, 16, 1024 * kQkCps);
       PieceIter qi;
-      qi.init(P.start, V, lo, hi);
+      pieces(qi);
       int v, x0, x1, piece = 0, jq = 0;
       uint32_t itq = 0;
       bool ok = true;
@@ -522,7 +569,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       const uint32_t idesc_pv = idesc_bf16_f32(128, 256, false, true);
       const uint64_t pv_desc = sw128_desc(sPv, kChunk, 1024);
       PieceIter vi;
-      vi.init(P.start, V, lo, hi);
+      pieces(vi);
       int v, x0, x1, piece = 0, jp = 0;
       uint32_t itv = 0;
       bool ok = true;
@@ -588,9 +635,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
     // token halves of the same rows; the two warps writing a page use the
     // halves q & 1 of the buffer, and each reader reads its partner's half
     const uint32_t x_slot = sX + (quad & 1) * 4096 + lane * 128;
-    float* red_sum = reinterpret_cast<float*>(smem_raw + (sX - smem_u32(smem_raw)));  // [4][64]
+    float* red_sum = &red_max[0][0];      // of the epilogue: no block is under way
+    const uint32_t sx_warp = sX + sw * 1024;      // epilogue: this warp's part of the exchange
     PieceIter pi;
-    pi.init(P.start, V, lo, hi);
+    pieces(pi);
     int v, x0, x1;
     int j = 0, pc = 0;
     bool dead = false;
@@ -788,27 +836,29 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
           // the whole virtual sequence: its rows are final
           const bool live = grow < vs.T * P.H;
           const long long row = (long long)vs.q0 * P.H + grow;
-          // All TMEM loads come before the rows part ways: a warp whose last
-          // rows lie past the chunk must not be split when it issues one.
-          uint32_t w[64];
-#pragma unroll
-          for (int cc = 0; cc < 4; ++cc) {
-            uint32_t r[32];
-            tmem_ld32(tmem + lane_addr + kTmemO + 128 * ch + 32 * cc, r);
+          const int r0 = 64 * (int)rank + 32 * (quad & 1);           // row of lane 0
+          const int valid = vs.T * P.H - vs.row0 - r0;
+          uint8_t* dst = reinterpret_cast<uint8_t*>(
+              P.o + ((long long)vs.q0 * P.H + vs.row0 + r0) * kDC + 256 * ch + 128 * hh);
+#pragma unroll 1
+          for (int cc = 0; cc < 2; ++cc) {
+            uint32_t ra[32], rb[32];
+            __syncwarp();
+            tmem_ld32(tmem + lane_addr + kTmemO + 128 * ch + 64 * cc, ra);
+            tmem_ld32(tmem + lane_addr + kTmemO + 128 * ch + 64 * cc + 32, rb);
             tmem_wait_ld();
+            uint32_t w[32];
 #pragma unroll
-            for (int i = 0; i < 16; ++i)
-              w[16 * cc + i] = pack_bf16x2(__uint_as_float(r[2 * i]) * inv,
-                                           __uint_as_float(r[2 * i + 1]) * inv);
+            for (int i = 0; i < 16; ++i) {
+              w[i] = pack_bf16x2(__uint_as_float(ra[2 * i]) * inv,
+                                 __uint_as_float(ra[2 * i + 1]) * inv);
+              w[16 + i] = pack_bf16x2(__uint_as_float(rb[2 * i]) * inv,
+                                      __uint_as_float(rb[2 * i + 1]) * inv);
+            }
+            store_rows32(sx_warp, w, dst + 128 * cc, kDC * 2, valid, lane);
           }
-          if (live) {
-            uint4* d4 = reinterpret_cast<uint4*>(P.o + row * kDC + 256 * ch + 128 * hh);
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-              d4[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            if (pb == 0)
-              P.lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
-          }
+          if (live && pb == 0)
+            P.lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
           __syncwarp();
           named_bar_sync(1, kSoftmaxThreads);  // red_sum is rewritten by the next piece
           tc_fence_before();
@@ -819,17 +869,17 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       }
       const long long slot = kRagged ? 2ll * worker + (x0 == 0 ? 1 : 0) : (long long)worker + v;
       const long long row = slot * 128 + 64 * (int)rank + h;
-      float* dst = P.ws_o + row * kDC + 256 * ch + 128 * hh;
+      uint8_t* dst = reinterpret_cast<uint8_t*>(
+          P.ws_o + (row - lane) * kDC + 256 * ch + 128 * hh);      // of lane 0's row
+#pragma unroll 1
       for (int cc = 0; cc < 4; ++cc) {
         uint32_t r[32];
+        __syncwarp();
         tmem_ld32(tmem + lane_addr + kTmemO + 128 * ch + 32 * cc, r);
         tmem_wait_ld();
-        float4* d4 = reinterpret_cast<float4*>(dst + 32 * cc);
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-          d4[i] = make_float4(__uint_as_float(r[4 * i]) * inv, __uint_as_float(r[4 * i + 1]) * inv,
-                              __uint_as_float(r[4 * i + 2]) * inv,
-                              __uint_as_float(r[4 * i + 3]) * inv);
+        for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
+        store_rows32(sx_warp, r, dst + 128 * cc, kDC * 4, 32, lane);
       }
       if (pb == 0)
         P.ws_lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
