@@ -13,9 +13,21 @@
 // The tensor-core kernel is the decode's (decode_tc.cuh: pair MMAs, 128 query
 // rows per cluster, 256-token blocks), over another list of virtual
 // sequences.  Each chunk's T_b H rows are cut into blocks of 128; a block
-// visits only the token blocks that its last row sees.  All blocks of all
-// chunks are laid end to end and split evenly over one worker per pair of
-// SMs, so a batch of one long chunk and many short ones keeps every SM busy.
+// visits only the token blocks that its last row sees.  One worker per pair of
+// SMs takes a run of token blocks.  Opening a row block costs a worker about
+// kOpen token blocks of time (the last one's O leaves, a new Q comes, the
+// pipeline refills).
+//   * All blocks of all row blocks are laid end to end, kOpen more before each
+//     row block, and split evenly: one long chunk among many short ones keeps
+//     every SM busy, and short row blocks count what they cost (13 mixed
+//     chunks: the worker with five one-block row blocks took 67 us, the median
+//     43, when only the blocks counted).
+//   * With at least as many workers as row blocks, every worker may serve one
+//     row block instead: t is the least number with sum_v ceil(blocks_v / t)
+//     <= workers, and row block v is split over ceil(blocks_v / t) of them.
+//     Fewer row blocks are cut; the merge of cut ones costs about 2 blocks, so
+//     this is taken up to 2 above the even share (16 x 4 queries over 4096
+//     tokens: 18 against 15.6, 104 -> 92 us).
 //   * A worker's pieces that cover their virtual sequence whole are final:
 //     the epilogue writes bf16 rows and the LSE.  Only a worker's first and
 //     last piece can be partial, so 2 slots per worker hold all partial
@@ -70,10 +82,11 @@ __device__ __forceinline__ bool chunk_bad(const int32_t* cu_q, int b, int total_
 // of their token blocks.  A cu_q that breaks its rules anywhere gives no
 // blocks at all: chunks could overlap.  A sequence whose length is impossible
 // keeps its rows with nothing to see (one empty block), so that they come out
-// as 0 and -inf.  first: [B + 1], scratch for B > kPlanSeqs.  worker_v[k]: the
-// virtual sequence of worker k's first block.  cuts[k], k < G - 1: the virtual sequence that the boundary between workers k and k + 1
+// as 0 and -inf.  first: [B + 1], scratch for B > kPlanSeqs.  lo[k], k
+// <= G: worker k's first block; worker_v[k]: its virtual sequence.  cuts[k], k < G - 1: the virtual sequence that the boundary between workers k and k + 1
 // cuts (-1: none), with its first and last worker.
 constexpr int kPlanSeqs = 2048;
+constexpr int kOpen = 2;
 struct ChunkCut {
   int v, k0, k1, pad;
 };
@@ -82,8 +95,10 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
                                                           int total_q, int max_q, int max_tokens,
                                                           int V, int G, int32_t* first_global,
                                                           VSeq* vseq, int32_t* start,
-                                                          ChunkCut* cuts, int32_t* worker_v) {
+                                                          ChunkCut* cuts, int32_t* worker_v,
+                                                          int32_t* lo) {
   __shared__ int warp_sums[32];
+  __shared__ int aligned;              // t of the aligned split, or 0
   __shared__ int first_sh[kPlanSeqs + 1];
   pdl_launch();
   int32_t* first = B <= kPlanSeqs ? first_sh : first_global;
@@ -92,6 +107,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
   for (int b = threadIdx.x; b < B; b += 1024) wrong |= chunk_bad(cu_q, b, total_q, max_q);
   if (__syncthreads_or(wrong)) {
     for (int v = threadIdx.x; v <= V; v += 1024) start[v] = 0;
+    for (int k = threadIdx.x; k <= G; k += 1024) lo[k] = 0;
     if (threadIdx.x == 0) raise_flag(kFlagBounds);
     return;
   }
@@ -136,13 +152,85 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
   }
   if (threadIdx.x == 0) start[V] = blocks;
   __syncthreads();
-  const int workers = min(G, blocks);
+  if (blocks == 0) {                   // no queries
+    for (int k = threadIdx.x; k <= G; k += 1024) lo[k] = 0;
+    return;
+  }
+  // cost of everything, kOpen before each row block
+  const long long cost = (long long)blocks + (long long)kOpen * live;
+  constexpr int kMine = 4;             // row blocks per lane of the aligned split
+  if (threadIdx.x < 32) {
+    const int lane = threadIdx.x;
+    int t = 0;
+    if (live <= min(G, 32 * kMine)) {
+      // consecutive row blocks per lane, in registers
+      int nb[kMine], most = 0;
+#pragma unroll
+      for (int i = 0; i < kMine; ++i) {
+        const int v = kMine * lane + i;
+        nb[i] = v < live ? start[v + 1] - start[v] : 0;
+        most = max(most, nb[i]);
+      }
+      most = __reduce_max_sync(0xffffffffu, most);
+      int a = (blocks + G - 1) / G, z = most;      // the least t lies in [a, z]
+      while (a < z) {
+        const int mid = (a + z) >> 1;
+        int m = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) m += (nb[i] + mid - 1) / mid;
+        if ((int)__reduce_add_sync(0xffffffffu, m) <= G) z = mid; else a = mid + 1;
+      }
+      if (a + kOpen <= (cost + G - 1) / G + 2) {
+        t = a;
+        int m = 0;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) m += (nb[i] + t - 1) / t;
+        int k = m;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const int y = __shfl_up_sync(0xffffffffu, k, o);
+          if (lane >= o) k += y;
+        }
+        const int used = __shfl_sync(0xffffffffu, k, 31);
+        k -= m;
+#pragma unroll
+        for (int i = 0; i < kMine; ++i) {
+          const int v = kMine * lane + i, n = (nb[i] + t - 1) / t;
+          for (int j = 0; j < n; ++j) {
+            lo[k + j] = start[v] + (int)((long long)nb[i] * j / n);
+            worker_v[k + j] = v;
+            if (j + 1 < n) cuts[k + j] = ChunkCut{v, k, k + n - 1, 0};
+          }
+          k += n;
+        }
+        for (int j = used + lane; j <= G; j += 32) lo[j] = blocks;
+      }
+    }
+    if (lane == 0) aligned = t;
+  }
+  __syncthreads();
+  if (aligned > 0) return;
+  // boundary k lies at floor(k cost / workers): in row block v's part [c0, c1),
+  // at its start or kOpen blocks less into it
+  const long long workers = min(G, blocks);
+  for (int k = (int)workers + threadIdx.x; k <= G; k += 1024) lo[k] = blocks;
   for (int v = threadIdx.x; v < live; v += 1024) {
-    const int v0 = start[v], v1 = start[v + 1];
-    if (v1 <= v0) continue;
-    const int k0 = worker_of(v0, blocks, workers), k1 = worker_of(v1 - 1, blocks, workers);
+    const int v0 = start[v];
+    const long long c0 = v0 + (long long)kOpen * v;
+    const long long c1 = start[v + 1] + (long long)kOpen * (v + 1);
+    int k0 = -1, k1 = -1;              // first and last worker of a row block that is cut
+    for (long long k = (c0 * workers + cost - 1) / cost; k < workers; ++k) {
+      const long long at = k * cost / workers;
+      if (at >= c1) break;
+      const int x = (int)max(at - c0 - kOpen, 0ll);
+      lo[k] = v0 + x;
+      worker_v[k] = v;
+      if (x > 0) {
+        if (k0 < 0) k0 = (int)k - 1;
+        k1 = (int)k;
+      }
+    }
     for (int k = k0; k < k1; ++k) cuts[k] = ChunkCut{v, k0, k1, 0};
-    for (int k = worker_lo(k0, blocks, workers) < v0 ? k0 + 1 : k0; k <= k1; ++k) worker_v[k] = v;
   }
 }
 
@@ -224,7 +312,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse,
 struct ChunkLayout {
   long long V;
   int G;
-  size_t off_first, off_vseq, off_cuts, off_wv, off_lse, off_o, total;
+  size_t off_first, off_vseq, off_cuts, off_wv, off_lo, off_lse, off_o, total;
 };
 
 inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
@@ -236,7 +324,8 @@ inline ChunkLayout chunk_layout(long long total_q, int B, int H, int G) {
   c.off_vseq = c.off_first + up(sizeof(int32_t) * ((size_t)B + 1));
   c.off_cuts = c.off_vseq + up(sizeof(VSeq) * c.V);
   c.off_wv = c.off_cuts + up(sizeof(ChunkCut) * G);
-  c.off_lse = c.off_wv + up(sizeof(int32_t) * G);
+  c.off_lo = c.off_wv + up(sizeof(int32_t) * G);
+  c.off_lse = c.off_lo + up(sizeof(int32_t) * (G + 1));
   c.off_o = c.off_lse + up(sizeof(float) * 2 * G * 128);
   c.total = c.off_o + sizeof(float) * 2 * G * 128 * dtc::kDC;
   return c;
@@ -254,6 +343,7 @@ inline mla_status launch_chunk_tc_impl(
   VSeq* vseq = reinterpret_cast<VSeq*>(ws + c.off_vseq);
   ChunkCut* cuts = reinterpret_cast<ChunkCut*>(ws + c.off_cuts);
   int32_t* worker_v = reinterpret_cast<int32_t*>(ws + c.off_wv);
+  int32_t* lo = reinterpret_cast<int32_t*>(ws + c.off_lo);
   float* ws_lse = reinterpret_cast<float*>(ws + c.off_lse);
   float* ws_o = reinterpret_cast<float*>(ws + c.off_o);
   CUtensorMap tQ, tQK, tPV;
@@ -264,7 +354,7 @@ inline mla_status launch_chunk_tc_impl(
     return MLA_ERR_CUDA;
   chunk_plan_kernel<<<1, 1024, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
                                         (int)c.V, c.G, first, vseq, start, cuts,
-                                        worker_v);
+                                        worker_v, lo);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
   DecodeTcParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
@@ -281,6 +371,7 @@ inline mla_status launch_chunk_tc_impl(
   p.scale_log2 = scale * 1.4426950408889634f;
   p.vseq = vseq;
   p.worker_v = worker_v;
+  p.worker_lo = lo;
   p.V = (int)c.V;
   p.o = o;
   p.lse = lse;

@@ -151,6 +151,7 @@ struct DecodeTcParams {
   // ragged chunks only
   const VSeq* vseq;       // [V]
   const int32_t* worker_v;   // [G] virtual sequence of each worker's first block
+  const int32_t* worker_lo;  // [G + 1] first block of each worker
   int V;
   __nv_bfloat16* o;       // [total_q][H][512]
   float* lse;             // [total_q][H]
@@ -341,10 +342,14 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
   }
   const int V = kRagged ? P.V : P.B * P.R;
   const int total = P.start[V];
-  // (ragged: no more workers than blocks, so that none is empty)
-  const int G = kRagged ? min(P.G, total) : P.G;
-  const int lo = total > 0 && worker < G ? worker_lo(worker, total, G) : 0;
-  const int hi = total > 0 && worker < G ? worker_lo(worker + 1, total, G) : 0;
+  int lo = 0, hi = 0;
+  if constexpr (kRagged) {
+    lo = P.worker_lo[worker];
+    hi = P.worker_lo[worker + 1];
+  } else if (total > 0) {
+    lo = worker_lo(worker, total, P.G);
+    hi = worker_lo(worker + 1, total, P.G);
+  }
 
   // (a search over the prefix sums takes a trip to L2 per step)
   auto pieces = [&](PieceIter& it) {

@@ -119,6 +119,24 @@ def test_more_workers_than_blocks_and_many_sequences():
 
 
 @gpu
+def test_no_queries():
+    """Room for tokens, but no chunk brings any."""
+    d = dims("bf16", H=16)
+    pool, table, n_pages, _ = paged(np.random.default_rng(0), [70, 300], 576, torch.bfloat16)
+    q = torch.randn((5, 16, 576), device=DEV).bfloat16()
+    o, lse = call(d, q, i32([0, 0, 0]), 5, 3, pool, n_pages, table, i32([70, 300]))
+    assert status() == 0
+    assert (o == 5).all() and (lse == 5).all()
+
+
+@gpu
+def test_many_short_row_blocks_behind_a_long_one():
+    """Row blocks of one token block each, next to one of many: splits fall on row blocks' starts."""
+    run(128, [1, 40, 1], [20000, 40, 700], seed=11, which=lambda T: sorted({0, T // 2, T - 1}))
+    run(16, [7, 200, 64, 1], [12000, 200, 64, 1], seed=12, which=lambda T: sorted({0, T // 2, T - 1}))
+
+
+@gpu
 def test_peaked_scores():
     run(16, [9, 1], [600, 2000], seed=4, peak=6.0)
 
