@@ -47,7 +47,9 @@ namespace mla {
 // one per sequence.
 inline long long chunk_max_v(long long total_q, int B, int H) { return total_q * H / 128 + B; }
 
-// Block-wide exclusive prefix sum of one value per thread (1024 threads).
+constexpr int kPlanThreads = 256;
+
+// Block-wide exclusive prefix sum of one value per thread (kPlanThreads).
 __device__ __forceinline__ int block_exclusive(int x, int* warp_sums, int* total) {
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
   int inc = x;
@@ -58,15 +60,14 @@ __device__ __forceinline__ int block_exclusive(int x, int* warp_sums, int* total
   }
   if (lane == 31) warp_sums[w] = inc;
   __syncthreads();
-  const int mine = warp_sums[lane];
-  int all = mine;
+  int before = 0, all = 0;
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int y = __shfl_up_sync(0xffffffffu, all, o);
-    if (lane >= o) all += y;
+  for (int i = 0; i < kPlanThreads / 32; ++i) {
+    const int y = warp_sums[i];
+    before += i < w ? y : 0;
+    all += y;
   }
-  *total = __shfl_sync(0xffffffffu, all, 31);
-  const int before = __shfl_sync(0xffffffffu, all - mine, w);
+  *total = all;
   __syncthreads();
   return before + inc - x;
 }
@@ -90,29 +91,30 @@ constexpr int kOpen = 2;
 struct ChunkCut {
   int v, k0, k1, pad;
 };
-__global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
+__global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t* cu_q,
                                                           const int32_t* seq_lens, int B, int H,
                                                           int total_q, int max_q, int max_tokens,
                                                           int V, int G, int32_t* first_global,
                                                           VSeq* vseq, int32_t* start,
                                                           ChunkCut* cuts, int32_t* worker_v,
                                                           int32_t* lo) {
-  __shared__ int warp_sums[32];
+  __shared__ int warp_sums[kPlanThreads / 32];
+  __shared__ int start_sh[kPlanSeqs];  // start, where it fits
   __shared__ int aligned;              // t of the aligned split, or 0
   __shared__ int first_sh[kPlanSeqs + 1];
   pdl_launch();
   int32_t* first = B <= kPlanSeqs ? first_sh : first_global;
-  for (int k = threadIdx.x; k < G; k += 1024) cuts[k].v = -1;
+  for (int k = threadIdx.x; k < G; k += kPlanThreads) cuts[k].v = -1;
   bool wrong = false;
-  for (int b = threadIdx.x; b < B; b += 1024) wrong |= chunk_bad(cu_q, b, total_q, max_q);
+  for (int b = threadIdx.x; b < B; b += kPlanThreads) wrong |= chunk_bad(cu_q, b, total_q, max_q);
   if (__syncthreads_or(wrong)) {
-    for (int v = threadIdx.x; v <= V; v += 1024) start[v] = 0;
-    for (int k = threadIdx.x; k <= G; k += 1024) lo[k] = 0;
+    for (int v = threadIdx.x; v <= V; v += kPlanThreads) start[v] = 0;
+    for (int k = threadIdx.x; k <= G; k += kPlanThreads) lo[k] = 0;
     if (threadIdx.x == 0) raise_flag(kFlagBounds);
     return;
   }
   int base = 0;
-  for (int b0 = 0; b0 < B; b0 += 1024) {
+  for (int b0 = 0; b0 < B; b0 += kPlanThreads) {
     const int b = b0 + threadIdx.x;
     const int T = b < B ? cu_q[b + 1] - cu_q[b] : 0;
     int sum;
@@ -124,7 +126,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
   __syncthreads();
   const int live = base;    // <= V, as the chunks do not overlap
   int blocks = 0;
-  for (int v0 = 0; v0 < V; v0 += 1024) {
+  for (int v0 = 0; v0 < V; v0 += kPlanThreads) {
     const int v = v0 + threadIdx.x;
     int nb = 0;
     if (v < live) {
@@ -147,13 +149,20 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
     }
     int sum;
     const int off = block_exclusive(nb, warp_sums, &sum);
-    if (v < V) start[v] = blocks + off;
+    if (v < V) {
+      start[v] = blocks + off;
+      if (v < kPlanSeqs) start_sh[v] = blocks + off;
+    }
     blocks += sum;
   }
-  if (threadIdx.x == 0) start[V] = blocks;
+  if (threadIdx.x == 0) {
+    start[V] = blocks;
+    if (V < kPlanSeqs) start_sh[V] = blocks;
+  }
   __syncthreads();
+  const int32_t* first_block = V < kPlanSeqs ? start_sh : start;
   if (blocks == 0) {                   // no queries
-    for (int k = threadIdx.x; k <= G; k += 1024) lo[k] = 0;
+    for (int k = threadIdx.x; k <= G; k += kPlanThreads) lo[k] = 0;
     return;
   }
   // cost of everything, kOpen before each row block
@@ -168,7 +177,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
 #pragma unroll
       for (int i = 0; i < kMine; ++i) {
         const int v = kMine * lane + i;
-        nb[i] = v < live ? start[v + 1] - start[v] : 0;
+        nb[i] = v < live ? first_block[v + 1] - first_block[v] : 0;
         most = max(most, nb[i]);
       }
       most = __reduce_max_sync(0xffffffffu, most);
@@ -197,7 +206,7 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
         for (int i = 0; i < kMine; ++i) {
           const int v = kMine * lane + i, n = (nb[i] + t - 1) / t;
           for (int j = 0; j < n; ++j) {
-            lo[k + j] = start[v] + (int)((long long)nb[i] * j / n);
+            lo[k + j] = first_block[v] + (int)((long long)nb[i] * j / n);
             worker_v[k + j] = v;
             if (j + 1 < n) cuts[k + j] = ChunkCut{v, k, k + n - 1, 0};
           }
@@ -213,11 +222,11 @@ __global__ void __launch_bounds__(1024) chunk_plan_kernel(const int32_t* cu_q,
   // boundary k lies at floor(k cost / workers): in row block v's part [c0, c1),
   // at its start or kOpen blocks less into it
   const long long workers = min(G, blocks);
-  for (int k = (int)workers + threadIdx.x; k <= G; k += 1024) lo[k] = blocks;
-  for (int v = threadIdx.x; v < live; v += 1024) {
-    const int v0 = start[v];
+  for (int k = (int)workers + threadIdx.x; k <= G; k += kPlanThreads) lo[k] = blocks;
+  for (int v = threadIdx.x; v < live; v += kPlanThreads) {
+    const int v0 = first_block[v];
     const long long c0 = v0 + (long long)kOpen * v;
-    const long long c1 = start[v + 1] + (long long)kOpen * (v + 1);
+    const long long c1 = first_block[v + 1] + (long long)kOpen * (v + 1);
     int k0 = -1, k1 = -1;              // first and last worker of a row block that is cut
     for (long long k = (c0 * workers + cost - 1) / cost; k < workers; ++k) {
       const long long at = k * cost / workers;
@@ -352,7 +361,7 @@ inline mla_status launch_chunk_tc_impl(
   if (cudaFuncSetAttribute(decode_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
-  chunk_plan_kernel<<<1, 1024, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
+  chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
                                         (int)c.V, c.G, first, vseq, start, cuts,
                                         worker_v, lo);
   if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
