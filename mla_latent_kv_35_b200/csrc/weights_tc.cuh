@@ -56,6 +56,12 @@ constexpr int kEpiWarp0 = 4;
 constexpr int kEpiThreads = 256;
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 9;
+// Pages that the start of a sequence counts for in the split of resident
+// queries: its queries are loaded and one more partial tile is worked.
+#ifndef MLA_WEIGHTS_OPEN
+#define MLA_WEIGHTS_OPEN 3
+#endif
+constexpr int kOpenPages = MLA_WEIGHTS_OPEN;
 #ifndef MLA_WEIGHTS_CHUNKS
 #define MLA_WEIGHTS_CHUNKS 3
 #endif
@@ -110,6 +116,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   __shared__ __align__(16) float lse2_sh[2][kN];
   __shared__ __align__(16) int lim_sh[2][kN];
   __shared__ float red[2][128];
+  __shared__ uint32_t odd_sh[2];           // refresh (from 1) whose rows were not all finite
   __shared__ long long sums[kThreads / 32], run_sh[3];
   __shared__ uint32_t tmem_base_sh;
   __shared__ int abort_flag;
@@ -137,6 +144,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     fence_mbar_init();
     tma_prefetch_desc(&tmQ);
     tma_prefetch_desc(&tmK);
+    odd_sh[0] = odd_sh[1] = 0;
     run_sh[0] = P.B;
     run_sh[1] = 0;
     run_sh[2] = 0;
@@ -147,6 +155,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   }
 
   // ---- this pair's run: first sequence, first tile, cost at its end ----
+  constexpr int kOpen = kQStat ? kOpenPages : 0;
   bool wrong = false;
   long long mine = 0;
   int u_first = 0, c_first = 1;          // of the thread's first sequence
@@ -154,7 +163,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     wrong |= chunk_bad(P.cu_q, b, P.total_q, P.max_q);
     int units;
     const int c = weights_units<kQStat, kN>(P, b, units);
-    mine += (long long)units * c;
+    mine += (long long)units * c + (units > 0 ? kOpen : 0);
     if (b < kThreads) {
       u_first = units;
       c_first = c;
@@ -187,7 +196,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
         units = 0;
         if (b < P.B) c = weights_units<kQStat, kN>(P, b, units);
       }
-      const long long x = (long long)units * c;
+      const long long x = (long long)units * c + (units > 0 ? kOpen : 0);
       long long inc = x;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -206,10 +215,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       // the first unit at or past lo: in this sequence, or at the start of a
       // later one
       if (x > 0 && at <= lo && lo < at + x) {
-        const long long t = (lo - at + c - 1) / c;
+        const long long t = (max(lo - at - kOpen, 0ll) + c - 1) / c;
         run_sh[0] = t < units ? b : b + 1;
         run_sh[1] = t < units ? t : 0;
-        run_sh[2] = t < units ? at + t * c : at + x;
+        run_sh[2] = t < units ? at + kOpen + t * c : at + x;
       }
       before += all;
     }
@@ -227,6 +236,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     int T, L, q0, blocks;    // its queries, length, first query token, row blocks (0: no queries)
     int page, pages;         // this tile: first page, pages (1 .. 4)
     bool last;               // the last tile of this sequence in the run
+    bool first;              // the run's first sequence: its start is in cost
     long long cost, hi;
   };
   // the next tile; false at the end of the run
@@ -238,6 +248,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
         w.T = P.cu_q[w.b + 1] - w.q0;
         w.L = P.seq_lens[w.b];
         if (w.T == 0) w.blocks = 0;
+        if (!w.first && w.units > 0) w.cost += kOpen;
+        w.first = false;
+        if (w.cost >= w.hi) return false;
       }
       if (w.x < w.units) {
         if constexpr (kQStat) {
@@ -265,6 +278,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
   w0.x = (int)run_sh[1];
   w0.units = -1;
   w0.cost = run_sh[2];
+  w0.first = true;
   w0.hi = hi > lo ? hi : 0;
   // pool page of page i (0, 1) of this CTA's half of the tile; -1: the tile
   // ends before it, n_pages: its id lies outside the pool (the box reads zeros)
@@ -462,30 +476,47 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
       const bool store = ch == 0 && k < w.pages && t < w.L;
       float acc = 0.f, old = 0.f;
       if (store && P.w_in != nullptr && P.keep != 0.f && t < w.L - w.T) old = P.w_in[at];
+      // lse of row r = et (+ kEpiThreads) of a row block, in units of log2;
+      // +inf for a row that gives nothing
+      constexpr int kRowsMine = (kN + kEpiThreads - 1) / kEpiThreads;
+      auto row_lse = [&](int rb, float (&v)[kRowsMine]) {
+#pragma unroll
+        for (int i = 0; i < kRowsMine; ++i) {
+          const int r = rb * kN + et + i * kEpiThreads;
+          v[i] = INFINITY;
+          if (et + i * kEpiThreads < kN && r < w.T * P.H) {
+            const float x = P.lse[(long long)w.q0 * P.H + r];
+            if (x > -INFINITY) v[i] = x * 1.4426950408889634f;
+          }
+        }
+      };
+      float next[kRowsMine];
+      if (steps > 0 && (!kQStat || loaded != w.b)) row_lse(0, next);
       for (int rb = 0; rb < steps; ++rb, ++j) {
-        // the rows' lse (in units of log2; +inf for a row that gives nothing)
-        // and visible limits.  Two sets in turn: the barrier of the next
-        // refresh keeps a set from being rewritten while it is read.
+        // the rows' lse and visible limits.  Two sets in turn: the barrier of
+        // the next refresh keeps a set from being rewritten while it is read.
+        // The next row block's are on their way meanwhile.
         if (!kQStat || loaded != w.b) {
-          const int rows = w.T * P.H - rb * kN;
-          for (int r = et; r < kN; r += kEpiThreads) {
-            float v = INFINITY;
-            int lim = 0;
-            if (r < rows) {
-              const float x = P.lse[(long long)w.q0 * P.H + rb * kN + r];
-              if (x > -INFINITY) v = x * 1.4426950408889634f;
-              lim = w.L - w.T + (rb * kN + r) / P.H + 1;
-            }
-            lse2_sh[refresh & 1][r] = v;
-            lim_sh[refresh & 1][r] = lim;
+#pragma unroll
+          for (int i = 0; i < kRowsMine; ++i) {
+            const int r = et + i * kEpiThreads;
+            if (r >= kN) break;
+            lse2_sh[refresh & 1][r] = next[i];
+            lim_sh[refresh & 1][r] = w.L - w.T + (rb * kN + r) / P.H + 1;
+            if (!(next[i] < INFINITY)) odd_sh[refresh & 1] = refresh + 1;
           }
           ++refresh;
           loaded = w.b;
           leave = named_bar_or(1, kEpiThreads, dead || *abort_p != 0);
           if (leave) break;
+          if (rb + 1 < steps) row_lse(rb + 1, next);
         }
         const float* l2 = lse2_sh[(refresh - 1) & 1] + (kN / 2) * ch;
         const int* lim = lim_sh[(refresh - 1) & 1] + (kN / 2) * ch;
+        // every row counts and sees the whole tile (the block's first row sees
+        // the least)
+        const bool plain = odd_sh[(refresh - 1) & 1] != refresh &&
+                           (w.page + w.pages) * kPage <= w.L - w.T + rb * kN / P.H + 1;
         const int buf = j % S::kBufs;
         const bool got = mbar_wait(smem_u32(&s_full[buf]), (j / S::kBufs) & 1, abort_p, 45, j);
         if (!__all_sync(0xffffffffu, got)) {
@@ -501,18 +532,22 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
           __syncwarp();
           tmem_ld32(sa + 32 * g, r);
           tmem_wait_ld();
+          if (plain) {
 #pragma unroll
-          for (int c = 0; c < 32; c += 4) {
-            const float4 l = *reinterpret_cast<const float4*>(l2 + 32 * g + c);
-            const int4 m = *reinterpret_cast<const int4*>(lim + 32 * g + c);
-            const float p0 = ex2_approx(fmaf(__uint_as_float(r[c]), P.scale_log2, -l.x));
-            const float p1 = ex2_approx(fmaf(__uint_as_float(r[c + 1]), P.scale_log2, -l.y));
-            const float p2 = ex2_approx(fmaf(__uint_as_float(r[c + 2]), P.scale_log2, -l.z));
-            const float p3 = ex2_approx(fmaf(__uint_as_float(r[c + 3]), P.scale_log2, -l.w));
-            s4[0] += t < m.x && l.x < INFINITY ? p0 : 0.f;
-            s4[1] += t < m.y && l.y < INFINITY ? p1 : 0.f;
-            s4[2] += t < m.z && l.z < INFINITY ? p2 : 0.f;
-            s4[3] += t < m.w && l.w < INFINITY ? p3 : 0.f;
+            for (int c = 0; c < 32; c += 4) {
+              const float4 l = *reinterpret_cast<const float4*>(l2 + 32 * g + c);
+              s4[0] += ex2_approx(fmaf(__uint_as_float(r[c]), P.scale_log2, -l.x));
+              s4[1] += ex2_approx(fmaf(__uint_as_float(r[c + 1]), P.scale_log2, -l.y));
+              s4[2] += ex2_approx(fmaf(__uint_as_float(r[c + 2]), P.scale_log2, -l.z));
+              s4[3] += ex2_approx(fmaf(__uint_as_float(r[c + 3]), P.scale_log2, -l.w));
+            }
+          } else {
+#pragma unroll
+            for (int c = 0; c < 32; ++c) {
+              const float l = l2[32 * g + c];
+              const float p = ex2_approx(fmaf(__uint_as_float(r[c]), P.scale_log2, -l));
+              s4[c & 3] += t < lim[32 * g + c] && l < INFINITY ? p : 0.f;
+            }
           }
         }
         tc_fence_before();
