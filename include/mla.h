@@ -495,7 +495,8 @@ mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, 
  * new_pos: device int32 [B, stride], each may be NULL (new_pos NULL: positions
  * are not kept); entries < new_lens[b] of new_weights and new_pos are written.
  * new_weights may be weights, new_pos slot_pos, new_lens seq_lens.  budget:
- * device int32 [B], < 0 counts as 0.  stride >= every length.  B <= 65535.
+ * device int32 [B], < 0 counts as 0.  stride >= every length, at most 2^30; B
+ * <= 65535.
  * workspace: device, >= mla_cache_evict_workspace_size bytes, 256-byte
  * aligned, contents ignored.  A length outside [0, min(stride,
  * max_pages*page_size)] leaves that sequence as it was and raises

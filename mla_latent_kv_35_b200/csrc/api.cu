@@ -1014,8 +1014,8 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
                            const int32_t* budget, int n_sink, int n_recent, float* new_weights,
                            int32_t* new_pos, int32_t* new_lens, void* workspace, size_t ws_bytes,
                            void* stream) {
-  if (!dims_ok(dims) || B < 0 || B > 65535 || stride < 1 || n_pages < 1 || max_pages < 1 ||
-      n_sink < 0 || n_recent < 0)
+  if (!dims_ok(dims) || B < 0 || B > 65535 || stride < 1 || stride > kEvictMaxStride ||
+      n_pages < 1 || max_pages < 1 || n_sink < 0 || n_recent < 0)
     return MLA_ERR_INVALID_ARG;
   if ((long long)max_pages * dims->page_size > 0x7FFFFFFFll) return MLA_ERR_INVALID_ARG;
   if (fp8_rows && !fp8_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;

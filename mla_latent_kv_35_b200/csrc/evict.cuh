@@ -30,7 +30,7 @@
 //     and positions that stay where they are, and the new length.
 // evict_move_kernel: every warp takes an even share of all sequences' pairs
 // and copies row, weight and position, two rows in flight.  (A grid of blocks
-// per sequence left the SMs of the short ones idle: 115 us against 40 for 64
+// per sequence left the SMs of the short ones idle: 116 us against 33 for 64
 // ragged sequences.)
 //
 // Bound: the plan by latency (loads, then three to six cluster barriers), the
@@ -43,6 +43,7 @@ namespace mla {
 
 constexpr int kEvictThreads = 1024;
 constexpr int kEvictMaxCluster = 8;    // (16, beyond the portable size: 42 against 35 us)
+constexpr int kEvictMaxStride = 1 << 30;   // slots are counted in 32 bits, with room
 constexpr int kEvictBins = 2048;
 // Keys a thread can hold: 8 where that is enough (fewer instructions per
 // thread: with 1024 threads the plan is bound by instruction issue), else 16.

@@ -209,9 +209,10 @@ class MLADecodeLayer:
         if self.dims.dtype != "bf16" or self.cache_kind != "bf16":
             raise ValueError(f"{what} needs a bf16 layer and a bf16 cache")
 
-    def extend_buffers(self, B: int, T: int, max_q: int):
-        """Device buffers of one extend() of B sequences and T tokens."""
-        key = ("extend", B, T, max_q)
+    def extend_buffers(self, B: int, T: int, max_q: int, slot: int = 0):
+        """Device buffers of one extend() of B sequences and T tokens (slot:
+        an independent second set, for calls or captured graphs that overlap)."""
+        key = ("extend", B, T, max_q, slot)
         if key not in self._bufs:
             d = self.dims
             dev, dt, H = self.device, d.torch_dtype, d.n_heads
@@ -228,7 +229,7 @@ class MLADecodeLayer:
         return self._bufs[key]
 
     def extend(self, h, batch_idx, pos, cu_q, T: int, max_q: int, fused: bool = True,
-               places=None):
+               places=None, slot: int = 0):
         """One step of ragged chunks: sequence b brings the tokens cu_q[b] ..
         cu_q[b+1]-1 of h [T, d_model] (device, dims dtype), the last of its
         seq_lens[b] cached tokens.
@@ -245,7 +246,7 @@ class MLADecodeLayer:
         self._absorbed_only("extend")
         d = self.dims
         B = self.page_table.shape[0]
-        bf = self.extend_buffers(B, T, max_q)
+        bf = self.extend_buffers(B, T, max_q, slot)
         _b.mla_project(d, h, self.W_A0, bf["y"], T, d.d_model, self.Y)
         self._pre_attention(bf, batch_idx, pos, places, T, fused)
         _b.mla_chunk_attention(d, bf["qbuf"], cu_q, T, max_q, self.pool, self.n_pages,
@@ -265,7 +266,8 @@ class MLADecodeLayer:
                             self.n_pages, self.page_table, self.max_pages, self.seq_lens,
                             self.page_table.shape[0], weights, keep, weights, weights.shape[1])
 
-    def evict(self, weights, budget, n_sink: int = 0, n_recent: int = 0, slot_pos=None):
+    def evict(self, weights, budget, n_sink: int = 0, n_recent: int = 0, slot_pos=None,
+              slot: int = 0):
         """Cut every sequence to budget[b] tokens (int32 [B] device): those with
         the least gathered weight leave, the first n_sink and the last
         n_recent positions excepted, and the survivors behind the new end move
@@ -274,10 +276,11 @@ class MLADecodeLayer:
         follow positions) in place.  Any layer and cache kind.
 
         New tokens then go to the slots from seq_lens on (places of step() and
-        extend()) at their own positions."""
+        extend()) at their own positions.  No page may belong to two sequences.
+        slot: an independent second workspace."""
         d = self.dims
         B, width = weights.shape
-        key = ("evict", B, width)
+        key = ("evict", B, width, slot)
         if key not in self._bufs:
             self._bufs[key] = torch.empty((_b.mla_cache_evict_workspace_size(d, B, width),),
                                           dtype=torch.uint8, device=self.device)

@@ -219,7 +219,7 @@ def test_refused_on_the_host():
     assert call(nB=0, pool=0, ws=0) == 0
     for kw in (dict(pool=0), dict(pt=0), dict(sl=0), dict(w=0), dict(bud=0), dict(nw=0), dict(nl=0),
                dict(ws=0), dict(ws=x + 16), dict(wb=100), dict(nB=-1), dict(nB=65536), dict(stride=0),
-               dict(n_pages=0), dict(mp=0), dict(ns=-1), dict(nr=-1), dict(mp=1 << 30)):
+               dict(n_pages=0), dict(mp=0), dict(stride=(1 << 30) + 1), dict(ns=-1), dict(nr=-1), dict(mp=1 << 30)):
         assert call(**kw) == 1, kw
     assert call(fp8=1, d=dims("f32")) == 2
     assert call(fp8=1, d=dims("bf16", dc=256)) == 2
