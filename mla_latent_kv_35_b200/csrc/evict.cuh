@@ -165,7 +165,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   // keys of this thread's slots s0 + 32 i + lane, and bit i of `free_bits`
   // where that slot is free
   uint32_t key[kKeys];
-  uint32_t free_bits = 0;
+  uint32_t free_bits = 0, minus_bits = 0;      // minus_bits: -0, whose key is that of 0
   int p1 = Lc - a.n_recent;              // free positions: [n_sink, p1)
   auto free_at = [&](int t) {
     const int p = sp != nullptr ? sp[t] : t;
@@ -206,6 +206,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
       const bool in = s0 + 32 * i + lane < s1;
+      minus_bits |= (uint32_t)(key[i] == 0x80000000u) << i;
       key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
       pos[i] = in ? pos[i] : -1;
       mx = max(mx, pos[i]);
@@ -281,26 +282,35 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     if (nw != nullptr) nw[t] = w[t];
     if (np != nullptr) np[t] = sp != nullptr ? sp[t] : t;
   };
-  // those of all slots with a bit in `stay`, four loads in flight
+  // those of all slots with a bit in `stay`: the weight is its key again, but
+  // for a NaN
   auto keep_slots = [&](uint32_t stay) {
+    if (np != nullptr) {
 #pragma unroll
-    for (int i0 = 0; i0 < kKeys; i0 += 4) {
-      if (i0 >= groups) break;
-      float v[4];
-      int p[4];
+      for (int i0 = 0; i0 < kKeys; i0 += 4) {
+        if (i0 >= groups) break;
+        int p[4];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int t = min(s0 + 32 * (i0 + i) + lane, s1 - 1);
-        v[i] = nw != nullptr ? w[t] : 0.f;
-        p[i] = np != nullptr && sp != nullptr ? sp[t] : t;
-      }
-#pragma unroll
-      for (int i = 0; i < 4; ++i)
-        if (stay >> (i0 + i) & 1) {
-          const int t = s0 + 32 * (i0 + i) + lane;
-          if (nw != nullptr) nw[t] = v[i];
-          if (np != nullptr) np[t] = p[i];
+        for (int i = 0; i < 4; ++i) {
+          const int t = min(s0 + 32 * (i0 + i) + lane, s1 - 1);
+          p[i] = sp != nullptr ? sp[t] : t;
         }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (stay >> (i0 + i) & 1) np[s0 + 32 * (i0 + i) + lane] = p[i];
+      }
+    }
+    if (nw != nullptr) {
+#pragma unroll
+      for (int i = 0; i < kKeys; ++i) {
+        if (i >= groups) break;
+        if (stay >> i & 1) {
+          const int t = s0 + 32 * i + lane;
+          const uint32_t u = key[i] ^ ((key[i] >> 31) ? 0x80000000u : 0xFFFFFFFFu);
+          nw[t] = key[i] == 0xFFFFFFFFu ? w[t]
+                                        : __uint_as_float(u | ((minus_bits >> i & 1) << 31));
+        }
+      }
     }
   };
   const uint32_t lower = (1u << lane) - 1;
@@ -333,32 +343,74 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     auto front_of = [&](int i) { return i < gf ? 0xffffffffu : i == gf ? edge : 0u; };
     auto run_of = [&](int i) { return i == groups - 1 ? tail : 0xffffffffu; };
     // ---- ranks of the vacated and the moving slots ----
-    int eq = eq0;
+    // Lane i keeps the leaving slots of group i0 + i as a mask, so that a warp
+    // scans 32 groups at once; the masks of the first 32 serve both passes.
+    auto masks = [&](int i0, int& eq) {
+      uint32_t mine = 0;
+      if (i0 == 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          if (i < groups) {
+            const uint32_t out = leaving(key[i], (free_bits >> i & 1) != 0, eq);
+            mine = lane == i ? out : mine;
+          }
+      }
+      for (int i = max(i0, kKeys); kRest && i < min(groups, i0 + 32); ++i) {
+        const int t = s0 + 32 * i + lane;
+        const uint32_t out =
+            leaving(t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t), eq);
+        mine = lane == i - i0 ? out : mine;
+      }
+      return mine;
+    };
+    int eq = eq0, eq_first = 0;
+    uint32_t first_masks = 0;
     int2 c = make_int2(0, 0);
-    each([&](int i, uint32_t k, bool fr) {
-      const uint32_t out = leaving(k, fr, eq), front = front_of(i);
+    for (int i0 = 0; i0 < groups; i0 += 32) {
+      const uint32_t out = masks(i0, eq), front = front_of(i0 + lane);
+      const uint32_t in = i0 + lane < groups ? run_of(i0 + lane) : 0u;
+      if (i0 == 0) {
+        first_masks = out;
+        eq_first = eq;
+      }
       c.x += __popc(out & front);
-      c.y += __popc(run_of(i) & ~out & ~front);
-    });
+      c.y += __popc(in & ~out & ~front);
+    }
+    c.x = __reduce_add_sync(0xffffffffu, c.x);
+    c.y = __reduce_add_sync(0xffffffffu, c.y);
     int2 sum, at = evict_scan(&scan_out, c, warp, lane, rank, n, &sum);
     n_hole = sum.x;
     int2* pairs = a.pairs + b * a.stride;
-    eq = eq0;
+    eq = eq_first;
     uint32_t stay = 0;          // bit i: slot i of this thread stays where it is
-    each([&](int i, uint32_t k, bool fr) {
-      const int t = s0 + 32 * i + lane;
-      const uint32_t out = leaving(k, fr, eq), front = front_of(i);
-      const uint32_t h = out & front, m = run_of(i) & ~out & ~front;
-      if (h >> lane & 1) pairs[at.x + __popc(h & lower)].x = t;
-      if (m >> lane & 1) pairs[at.y + __popc(m & lower)].y = t;
-      at.x += __popc(h);
-      at.y += __popc(m);
-      const bool stays = (run_of(i) & front & ~out) >> lane & 1;
-      if (i < kKeys)
-        stay |= (uint32_t)stays << i;
-      else if (stays)
-        keep_slot(t);
-    });
+    for (int i0 = 0; i0 < groups; i0 += 32) {
+      const uint32_t out = i0 == 0 ? first_masks : masks(i0, eq), front = front_of(i0 + lane);
+      const uint32_t in = i0 + lane < groups ? run_of(i0 + lane) : 0u;
+      const uint32_t hole = out & front, move = in & ~out & ~front, here = in & ~out & front;
+      const int ih = warp_inclusive(__popc(hole), lane), im = warp_inclusive(__popc(move), lane);
+      const int oh = at.x + ih - __popc(hole), om = at.y + im - __popc(move);
+      const int end = min(32, groups - i0);
+      for (int i = 0; i < end; ++i) {
+        const int t = s0 + 32 * (i0 + i) + lane;
+        const uint32_t h = __shfl_sync(0xffffffffu, hole, i);
+        const uint32_t m = __shfl_sync(0xffffffffu, move, i);
+        if (h != 0) {
+          const int o = __shfl_sync(0xffffffffu, oh, i);
+          if (h >> lane & 1) pairs[o + __popc(h & lower)].x = t;
+        }
+        if (m != 0) {
+          const int o = __shfl_sync(0xffffffffu, om, i);
+          if (m >> lane & 1) pairs[o + __popc(m & lower)].y = t;
+        }
+        const bool stays = __shfl_sync(0xffffffffu, here, i) >> lane & 1;
+        if (i0 + i < kKeys)
+          stay |= (uint32_t)stays << i;
+        else if (stays)
+          keep_slot(t);
+      }
+      at.x += __shfl_sync(0xffffffffu, ih, 31);
+      at.y += __shfl_sync(0xffffffffu, im, 31);
+    }
     keep_slots(stay);
   } else {
     for (int t = s0 + lane; t < s1; t += 32) keep_slot(t);
