@@ -166,10 +166,10 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   // where that slot is free
   uint32_t key[kKeys];
   uint32_t free_bits = 0, minus_bits = 0;      // minus_bits: -0, whose key is that of 0
-  int p1 = Lc - a.n_recent;              // free positions: [n_sink, p1)
+  int last = Lc - 1 - a.n_recent;        // free positions: [n_sink, last]
   auto free_at = [&](int t) {
     const int p = sp != nullptr ? sp[t] : t;
-    return p >= a.n_sink && p < p1;
+    return p >= a.n_sink && p <= last;
   };
   // f(i, key, free) over this thread's groups; key and free of a slot past the
   // run are 0 and false
@@ -221,11 +221,11 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
       mx = max_sh;
       if (n > 1)
         for (uint32_t r = 0; r < n; ++r) mx = max(mx, ld_cluster(smem_u32(&max_sh), r));
-      p1 = mx + 1 - a.n_recent;
+      last = mx - a.n_recent;
     }
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
-      if (pos[i] >= a.n_sink && pos[i] < p1) free_bits |= 1u << i;
+      if (pos[i] >= a.n_sink && pos[i] <= last) free_bits |= 1u << i;
 
     // ---- the n_out-th smallest key, digit by digit ----
 #pragma unroll
