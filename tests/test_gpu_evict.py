@@ -109,6 +109,16 @@ def test_small_lengths(kind, placed):
 
 
 @gpu
+@pytest.mark.parametrize("n_recent", [0, 1, 7, 2 ** 31 - 1])
+def test_the_last_position_there_is(n_recent):
+    rng = np.random.default_rng(12)
+    lens = [40, 9000]
+    pos = [2 ** 31 - 1 - rng.permutation(2 * L)[:L] for L in lens]
+    pos[0][5] = 2 ** 31 - 1
+    run(dims("bf16"), lens, [10, 4000], draw_w(rng, lens, "spread"), pos, 3, n_recent)
+
+
+@gpu
 @pytest.mark.parametrize("stride", [4096, 4097, 9000, 20000, 70000])
 @pytest.mark.parametrize("kind", ["spread", "ties", "odd"])
 def test_clusters(stride, kind):
