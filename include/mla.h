@@ -397,7 +397,8 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
  * mla_chunk_attention_workspace_size bytes, 256-byte aligned, contents
  * ignored.  qbuf, pool and o_lat 16-byte aligned.  Needs dtype MLA_BF16,
  * d_latent == 512, d_rope == 64, page_size == 64 (else MLA_ERR_UNSUPPORTED,
- * workspace size 0), any n_heads, total_q * H + 128 * B < 2^31.  A cu_q that
+ * workspace size 0), any n_heads, total_q * H + 128 * B < 2^31, and
+ * (total_q * H / 128 + B) * (max_pages / 4, rounded up) < 2^31.  A cu_q that
  * breaks its rules anywhere leaves every row as it was; a chunk with L < T_b
  * or L > max_pages*page_size gets o_lat = 0, lse = -inf; both raise
  * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as
@@ -424,7 +425,8 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
  * entries from L on are left as they were.  A row with lse = -inf gives
  * nothing.  Products of bf16 accumulate in fp32, the sums are fp32 in a fixed
  * order (the same bits every time).  Shapes, checks and cu_q as for
- * mla_chunk_attention; stride >= every length, keep finite.  A cu_q that
+ * mla_chunk_attention, but for its last bound, in place of which max_pages *
+ * page_size < 2^31 - 256; stride >= every length, keep finite.  A cu_q that
  * breaks its rules leaves w_out as it was; so does, for its sequence, a
  * length < T_b or > min(stride, max_pages*page_size); both raise
  * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as

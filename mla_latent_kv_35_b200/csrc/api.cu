@@ -771,7 +771,7 @@ mla_status mla_out_proj_bf16(const mla_dims* dims, const void* o_lat, const void
   if (dims->dtype != MLA_BF16) return MLA_ERR_UNSUPPORTED;
   if (T == 0) return MLA_OK;
   if (!o_lat || !w_uv || !w_o || !scratch || !out) return MLA_ERR_INVALID_ARG;
-  if (scratch_bytes < mla_out_proj_bf16_scratch_size(dims, T) ||
+  if (!aligned16(o_lat) || scratch_bytes < mla_out_proj_bf16_scratch_size(dims, T) ||
       (reinterpret_cast<uintptr_t>(scratch) & 255u) != 0)
     return MLA_ERR_INVALID_ARG;
   return out_proj_bf16(dims, static_cast<const __nv_bfloat16*>(o_lat), w_uv, w_o,
@@ -869,6 +869,15 @@ static bool chunk_sizes_ok(const mla_dims* d, int B, int total_q, int max_q) {
          (long long)total_q * d->n_heads + 128LL * B < 0x7FFFFFFFll;
 }
 
+// Token blocks of a call are counted in 32 bits, row blocks times those of a
+// full page table at most; lengths leave room to be rounded up to a block.
+static bool chunk_pages_ok(const mla_dims* d, int B, int total_q, int max_pages) {
+  const long long tokens = (long long)max_pages * d->page_size;
+  return max_pages >= 1 && tokens <= 0x7FFFFFFFll - dtc::kBlk &&
+         chunk_max_v(total_q, B, d->n_heads) * ((tokens + dtc::kBlk - 1) / dtc::kBlk) <
+             0x7FFFFFFFll;
+}
+
 size_t mla_chunk_attention_workspace_size(const mla_dims* dims, int B, int total_q, int max_q) {
   if (!dims_ok(dims) || !chunk_dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q)) return 0;
   return chunk_layout(total_q, B, dims->n_heads, sm_count() / 2).total;
@@ -879,8 +888,8 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
                                const int32_t* page_table, int max_pages, const int32_t* seq_lens,
                                int B, void* workspace, size_t ws_bytes, void* o_lat, float* lse,
                                void* stream) {
-  if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 || max_pages < 1 ||
-      (long long)max_pages * dims->page_size > 0x7FFFFFFFll)
+  if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 ||
+      !chunk_pages_ok(dims, B, total_q, max_pages))
     return MLA_ERR_INVALID_ARG;
   if (!chunk_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
   if (B == 0 || total_q == 0) return MLA_OK;
@@ -905,7 +914,8 @@ mla_status mla_attn_weights(const mla_dims* dims, const void* qbuf, const float*
                             const int32_t* seq_lens, int B, const float* w_in, float keep,
                             float* w_out, int stride, void* stream) {
   if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 || max_pages < 1 ||
-      (long long)max_pages * dims->page_size > 0x7FFFFFFFll || stride < 1 || !std::isfinite(keep))
+      (long long)max_pages * dims->page_size > 0x7FFFFFFFll - wtc::kTile || stride < 1 ||
+      !std::isfinite(keep))
     return MLA_ERR_INVALID_ARG;
   if (!chunk_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
   if (B == 0) return MLA_OK;

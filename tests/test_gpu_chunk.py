@@ -245,7 +245,8 @@ def test_refused_on_the_host():
     for kw in (dict(q=0), dict(cu=0), dict(pool=0), dict(pt=0), dict(sl=0), dict(ws=0), dict(o=0), dict(lse=0),
                dict(q=x + 2), dict(pool=x + 8), dict(o=x + 4), dict(ws=x + 128), dict(wb=1000), dict(nB=-1),
                dict(total=-1), dict(max_q=-1), dict(max_q=9), dict(n_pages=0), dict(mp=0),
-               dict(total=1 << 24), dict(mp=1 << 30)):
+               dict(total=1 << 24), dict(mp=1 << 30),
+               dict(mp=(1 << 25) - 1), dict(total=1 << 23, mp=1024)):
         assert f(**kw) == 1, kw
     for d in (dims("f32"), dims("bf16", dc=256), dims("bf16", dr=32), dims("bf16", page=32)):
         assert f(d=d) == 2
