@@ -67,6 +67,10 @@ class MLADims:
                     self.d_v, self.d_model, self.page_size, self.scale,
                     self.rope_base, MLA_BF16 if self.dtype == "bf16" else MLA_F32)
 
+    def __getstate__(self):
+        """Copies and pickles leave the cached C struct behind (_ref)."""
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
     @property
     def torch_dtype(self):
         return torch.bfloat16 if self.dtype == "bf16" else torch.float32

@@ -76,6 +76,19 @@ def test_evict_by_hand():
     assert oracle.evict([-0.0, 0.0, nan, 0.0], [0, 1, 2, 3], 3, 0, 0) == ([(0, 3)], 3)
 
 
+def test_dims_copy_and_pickle_after_their_first_call():
+    import copy
+    import pickle
+
+    from mla_latent_kv_35_b200 import binding, build
+    build.build()
+    d = binding.MLADims(8, 128, 512, 64, 128, 256, 64, 0.1, 10000.0, "bf16")
+    size = binding.mla_chunk_attention_workspace_size(d, 2, 8, 4)
+    for e in (copy.copy(d), copy.deepcopy(d), pickle.loads(pickle.dumps(d))):
+        assert e == d
+        assert binding.mla_chunk_attention_workspace_size(e, 2, 8, 4) == size
+
+
 @pytest.mark.parametrize("seed", range(20))
 def test_evict_keeps_the_heaviest_and_moves_the_fewest(seed):
     rng = np.random.default_rng(seed)
