@@ -466,7 +466,8 @@ mla_status mla_out_proj_bf16(const mla_dims* dims, const void* o_lat, const void
  * t*q_stride_tok + i*(d_nope+d_rope); qbuf: device [T, H, d_latent + d_rope];
  * ckr: device rows of d_latent + d_rope at stride ckr_stride_tok (what
  * mla_cache_append_fp8 takes).  q may be y, and ckr the end of y's rows
- * (y + H*(d_nope+d_rope)), with y's stride; no other overlap.  page_table:
+ * (y + H*(d_nope+d_rope)), with y's stride; no other overlap.  Of two tokens
+ * with the same slot, the row may mix both.  page_table:
  * device int32 [n_seqs, max_pages].  A sequence, slot or page outside them or
  * the pool skips that append and raises MLA_ERR_BOUNDS.  Both
  * dtypes, any widths; DeepSeek-V2's, 16-byte aligned, take the fast kernel. */

@@ -210,23 +210,32 @@ class MLADecodeLayer:
             raise ValueError(f"{what} needs a bf16 layer and a bf16 cache")
 
     def extend_buffers(self, B: int, T: int, max_q: int, slot: int = 0):
-        """Device buffers of one extend() of B sequences and T tokens (slot:
-        an independent second set, for calls or captured graphs that overlap)."""
-        key = ("extend", B, T, max_q, slot)
+        """Device buffers of one extend() of B sequences and T tokens, valid
+        until the next extend() of this slot (slot: an independent second set,
+        for calls or captured graphs that overlap).  They are views of sets
+        whose rows are powers of two: the number of tokens differs from step
+        to step, and the memory is at most that of four sets of the longest."""
+        rows = 1 << (T - 1).bit_length() if T > 0 else 1
+        key = ("extend", B, rows, slot)
         if key not in self._bufs:
             d = self.dims
             dev, dt, H = self.device, d.torch_dtype, d.n_heads
+            # (the output projection's split, and with it its scratch, may grow as T falls)
+            scratch = max(_b.mla_out_proj_bf16_scratch_size(d, t)
+                          for t in range(rows // 2 + 1, rows + 1))
             self._bufs[key] = dict(
-                y=torch.empty((T, self.Y), dtype=dt, device=dev),
-                qbuf=torch.empty((T, H, self.D), dtype=dt, device=dev),
-                o_lat=torch.empty((T, H, d.d_latent), dtype=dt, device=dev),
-                lse=torch.empty((T, H), dtype=torch.float32, device=dev),
-                out=torch.empty((T, d.d_model), dtype=torch.float32, device=dev),
-                ws=torch.empty((_b.mla_chunk_attention_workspace_size(d, B, T, max_q),),
+                y=torch.empty((rows, self.Y), dtype=dt, device=dev),
+                qbuf=torch.empty((rows, H, self.D), dtype=dt, device=dev),
+                o_lat=torch.empty((rows, H, d.d_latent), dtype=dt, device=dev),
+                lse=torch.empty((rows, H), dtype=torch.float32, device=dev),
+                out=torch.empty((rows, d.d_model), dtype=torch.float32, device=dev),
+                ws=torch.empty((_b.mla_chunk_attention_workspace_size(d, B, rows, rows),),
                                dtype=torch.uint8, device=dev),
-                scratch=torch.empty((_b.mla_out_proj_bf16_scratch_size(d, T),),
-                                    dtype=torch.uint8, device=dev))
-        return self._bufs[key]
+                scratch=torch.empty((scratch,), dtype=torch.uint8, device=dev))
+        full = self._bufs[key]
+        if rows == T:
+            return full
+        return {k: t if k in ("ws", "scratch") else t[:T] for k, t in full.items()}
 
     def extend(self, h, batch_idx, pos, cu_q, T: int, max_q: int, fused: bool = True,
                places=None, slot: int = 0):
@@ -236,7 +245,11 @@ class MLADecodeLayer:
 
         cu_q int32 [B+1] device, batch_idx and pos int32 [T] device, max_q >=
         the longest chunk; places as for step().  Decode tokens, speculative
-        tokens and prompt tails go through one call:
+        tokens and prompt tails go through one call.  Rows of h from cu_q[B]
+        on are padding (a captured graph replays with the chunks that cu_q then
+        holds): what out and o_lat hold for them is undefined, and their
+        batch_idx and places name a slot that holds no token (several may name
+        the same one).
 
           A0  mla_project, A1-A3 as in step(), mla_chunk_attention,
           mla_out_proj_bf16
@@ -356,12 +369,12 @@ class MLADecodeLayer:
         return bf
 
     def capture(self, h, batch_idx, pos, B: int, S_q: int, num_workers: int = 0,
-                fused: bool = True, slot: int = 0):
+                fused: bool = True, slot: int = 0, places=None):
         """Capture one step on these input buffers into a CUDA graph.
 
         Returns (graph, buffers, kernels): graph.replay() reruns the whole
         step (projection through output projection) on whatever h,
-        batch_idx and pos hold at that time, writing the same buffers;
+        batch_idx, pos and places hold at that time, writing the same buffers;
         kernels is the number of kernel launches the graph contains.  The
         step's buffers are allocated before capture, so the graph holds no
         memory of its own.
@@ -371,7 +384,7 @@ class MLADecodeLayer:
         graph = torch.cuda.CUDAGraph()
         l0 = _b.mla_launch_count()
         with torch.cuda.graph(graph):
-            self.step(h, batch_idx, pos, B, S_q, num_workers, fused, slot)
+            self.step(h, batch_idx, pos, B, S_q, num_workers, fused, slot, places)
         kernels = _b.mla_launch_count() - l0
         return graph, bf, kernels
 

@@ -283,6 +283,64 @@ def test_a_graph_of_a_step_with_its_weights_and_eviction():
 
 
 @gpu
+def test_a_graph_of_padded_chunks_and_buffers_of_many_lengths():
+    """One captured extend of 9 rows replays with the chunks that cu_q then holds (rows behind them
+    pad), as the eager call of just those rows; and steps of other lengths use few sets of buffers."""
+    T, n = 9, 3
+    layer, W, rng = make(norms=True, n_seqs=n, seed=5)
+    ctx = [30, 1, 200]
+    h_ctx = [q(rng.standard_normal((k, 256)), "bf16") for k in ctx]
+    layer.prefill_from_hidden(h_ctx)
+    ref = Reference(layer.dims, W, n)
+    rows = [ref.new_rows(x, np.arange(k))[1] for x, k in zip(h_ctx, ctx)]
+    start = layer.pool.clone()
+    spare = 500                                            # a slot that no sequence reaches
+    hd = torch.zeros((T, 256), dtype=torch.bfloat16, device=DEV)
+    bi, pos, places, cu = i32([0] * T), i32([0] * T), i32([spare] * T), i32([0] * (n + 1))
+    layer.extend(hd, bi, pos, cu, T, 5, places=places)     # allocates
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g, stream=side):
+        bf = layer.extend(hd, bi, pos, cu, T, 5, places=places)
+    for qs in ([5, 1, 3], [0, 0, 1], [2, 5, 0], [0, 0, 0], [1, 1, 1]):
+        k = sum(qs)
+        cum = np.concatenate([[0], np.cumsum(qs)])
+        p = np.concatenate([np.arange(c, c + m) for c, m in zip(ctx, qs)] + [np.full(T - k, spare)])
+        b = np.concatenate([np.repeat(np.arange(n), qs), np.zeros(T - k)])
+        h = q(rng.standard_normal((T, 256)), "bf16")
+        layer.seq_lens.copy_(i32(np.array(ctx) + qs))
+        layer.pool.copy_(start)
+        for t, x in ((hd, to_dev(h, "bf16")), (bi, i32(b)), (pos, i32(p)), (places, i32(p)), (cu, i32(cum))):
+            t.copy_(x)
+        g.replay()
+        got = [bf[name][:k].clone() for name in ("out", "o_lat", "lse")]
+        assert status() == 0
+        if k == 0:
+            continue
+        ref.rows = list(rows)
+        out, o, lse, _ = ref.extend(h[:k], cum, p[:k])
+        for unpadded in (False, True):
+            check(to_np(got[1]), o, "bf16", "o_lat", dict(max_abs=6e-2, mean_abs=6e-3, rel_l2=2e-2))
+            check(to_np(got[2]), lse, "bf16", "lse", dict(max_abs=6e-2, mean_abs=6e-3))
+            check(to_np(got[0]), out, "bf16", "out", dict(max_abs=6e-2, mean_abs=6e-3, rel_l2=2e-2))
+            if not unpadded:                               # the same rows alone, in buffers of their own
+                layer.pool.copy_(start)
+                one = layer.extend(hd[:k], bi[:k], pos[:k], cu, k, 5 if k > 5 else k, places=places[:k], slot=1)
+                assert [one[name].shape[0] for name in ("out", "o_lat", "lse", "y", "qbuf")] == [k] * 5
+                got = [one[name].clone() for name in ("out", "o_lat", "lse")]
+    assert status() == 0
+    before = torch.cuda.memory_allocated()
+    sets = {key[2] for key in layer._bufs if key[0] == "extend"}
+    for k in range(1, 17):
+        layer.extend_buffers(n, k, k)
+    assert {key[2] for key in layer._bufs if key[0] == "extend"} == sets | {1, 2, 4, 8, 16}
+    assert torch.cuda.memory_allocated() - before < 5 * 64 * 2 ** 20
+    layer.extend(hd[:0], bi, pos, cu * 0, 0, 0)            # no rows at all
+    assert status() == 0
+
+
+@gpu
 def test_refusals_of_the_layer():
     layer, W, rng = make(kind="fp8")
     with pytest.raises(ValueError):
