@@ -1011,11 +1011,11 @@ mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, 
 // ---------------------------------------------------------------------------
 // eviction by gathered attention weight
 // ---------------------------------------------------------------------------
-// Workspace: the pairs [B][stride], then their counts [B].
+// Workspace: the pairs [B][2][stride], then their counts [B].
 size_t mla_cache_evict_workspace_size(const mla_dims* dims, int B, int stride) {
   if (!dims_ok(dims) || B < 0 || stride < 1) return 0;
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
-  return up((size_t)B * stride * sizeof(int2)) + up((size_t)B * sizeof(int32_t));
+  return up((size_t)B * stride * 8) + up((size_t)B * sizeof(int32_t));
 }
 
 mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp8_rows,
@@ -1040,10 +1040,10 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   EvictArgs a{};
   a.seq_lens = seq_lens; a.budget = budget; a.weights = weights; a.slot_pos = slot_pos;
   a.new_weights = new_weights; a.new_pos = new_pos; a.new_lens = new_lens;
-  a.pairs = static_cast<int2*>(workspace);
+  a.pairs = static_cast<int32_t*>(workspace);
   a.n_pairs = reinterpret_cast<int32_t*>(
       static_cast<char*>(workspace) +
-      (((size_t)B * stride * sizeof(int2) + 255) & ~(size_t)255));
+      (((size_t)B * stride * 8 + 255) & ~(size_t)255));
   a.stride = stride;
   a.max_tokens = max_pages * dims->page_size;
   a.n_sink = n_sink; a.n_recent = n_recent;
@@ -1086,7 +1086,7 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   at[0].val.programmaticStreamSerializationAllowed = 1;
   mv.attrs = at;
   mv.numAttrs = 1;
-  const int2* pairs = a.pairs;
+  const int32_t* pairs = a.pairs;
   const int32_t* n_pairs = a.n_pairs;
   const cudaError_t moved =
       row_bytes % 16 == 0 && aligned16(pool)

@@ -15,10 +15,13 @@
 //   * Weights are compared as 32-bit keys that order like the floats (-0 as
 //     0; NaN behind +inf, so a NaN weight is kept longest).  Three passes of
 //     11, 11 and 10 bits find the n_out-th smallest key: a histogram of the
-//     digit in shared memory, summed over the cluster's blocks through
-//     distributed shared memory, then a scan for the digit that holds the
-//     rank.  Nothing is sorted.  The first pass's sum is the number of free
-//     slots, so it needs no count of its own.
+//     digit in shared memory, then one warp finds the digit that holds the
+//     rank, first among sums of 64 bins, then among the 64, each summed over
+//     the cluster's blocks through distributed shared memory (32 + 64 words of
+//     every block; reading all 2048 bins took 4000 clocks a pass against 1600
+//     with eight blocks).  Nothing is sorted.  The first pass's sum is the number of free
+//     slots, so it needs no count of its own.  Where all keys that share the
+//     digits found so far leave, the remaining passes are left out.
 //   * Every warp owns one run of consecutive slots, 32 at a time, and keeps
 //     their keys in registers (up to 16 per thread; each pass reads the
 //     weights of a longer run's rest again).  Ranks
@@ -26,15 +29,19 @@
 //     block and one exchange per cluster.
 //   * Among equal keys the lowest slots leave.  Their ranks take another
 //     exchange, made only where some of the equal ones stay.
-//   * It writes the pairs (vacated slot, moving slot), the survivors' weights
-//     and positions that stay where they are, and the new length.
+//   * It writes the vacated and the moving slots, the weights and positions
+//     before the new end, and the new length.  Those of a vacated slot are
+//     written too, while they are at hand, since the move overwrites them.
 // evict_move_kernel: every warp takes an even share of all sequences' pairs
 // and copies row, weight and position, two rows in flight.  (A grid of blocks
 // per sequence left the SMs of the short ones idle: 116 us against 33 for 64
 // ragged sequences.)
 //
-// Bound: the plan by latency (loads, then three to six cluster barriers), the
-// move by memory bandwidth.
+// Bound: the plan by latency (loads, then three to six cluster barriers) and by
+// instruction issue (32 warps on one SM), the move by memory bandwidth.
+// Measured in a graph: one token of 16 x 4097 12.9 us (plan 9.5), 64 sequences
+// of 129 to 32769 tokens to 30 % 55 us (plan 18.5), 4 x 131072 halved 78 us
+// (plan 21).
 #pragma once
 
 #include "common.cuh"
@@ -58,17 +65,18 @@ struct EvictArgs {
   float* new_weights;         // [B][stride], may be weights
   int32_t* new_pos;           // [B][stride], may be slot_pos; nullptr: not kept
   int32_t* new_lens;          // [B], may be seq_lens
-  int2* pairs;                // [B][stride]: (to, from)
+  int32_t* pairs;             // [B][2][stride]: vacated slots, moving slots
   int32_t* n_pairs;           // [B]
   long long stride;
   int max_tokens;             // max_pages * page_size
   int n_sink, n_recent;
 };
 
-// key order: -inf < ... < -0 = 0 < ... < +inf < NaN
+// key order: -inf < ... < -0 = 0 < ... < +inf < NaN < a slot that is not free
+constexpr uint32_t kEvictKept = 0xFFFFFFFFu;
 __device__ __forceinline__ uint32_t evict_key(float w) {
   uint32_t u = __float_as_uint(w);
-  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return 0xFFFFFFFFu;
+  if ((u & 0x7FFFFFFFu) > 0x7F800000u) return kEvictKept - 1;
   if ((u & 0x7FFFFFFFu) == 0) u = 0;
   return u ^ ((u >> 31) ? 0xFFFFFFFFu : 0x80000000u);
 }
@@ -85,8 +93,24 @@ __device__ __forceinline__ int ld_cluster(uint32_t addr, uint32_t rank) {
   return v;
 }
 
+// Sum of the words at `p` over the cluster's n blocks, all remote reads in
+// flight at once: one takes about 600 clocks.
+__device__ __forceinline__ int cluster_sum(const int* p, uint32_t n) {
+  if (n == 1) return *p;
+  int sum = 0, v[kEvictMaxCluster];
+#pragma unroll
+  for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
+    v[r] = 0;
+    if (r < n)
+      asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v[r]) : "r"(mapa_shared(smem_u32(p), r)));
+  }
+#pragma unroll
+  for (uint32_t r = 0; r < kEvictMaxCluster; ++r) sum += v[r];
+  return sum;
+}
+
 // The pair of words at `addr` in every block of the cluster (zeros past the
-// n-th), all loads in flight at once: one remote read takes about 600 clocks.
+// n-th).
 __device__ __forceinline__ void ld_cluster_all(uint32_t addr, uint32_t n,
                                                int2 (&v)[kEvictMaxCluster]) {
 #pragma unroll
@@ -97,6 +121,17 @@ __device__ __forceinline__ void ld_cluster_all(uint32_t addr, uint32_t n,
                    : "=r"(v[r].x), "=r"(v[r].y)
                    : "r"(mapa_shared(addr, r)));
   }
+}
+__device__ __forceinline__ int2 cluster_sum(const int2* p, uint32_t n) {
+  if (n == 1) return *p;
+  int2 sum = make_int2(0, 0), v[kEvictMaxCluster];
+  ld_cluster_all(smem_u32(p), n, v);
+#pragma unroll
+  for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
+    sum.x += v[r].x;
+    sum.y += v[r].y;
+  }
+  return sum;
 }
 
 __device__ __forceinline__ int warp_inclusive(int x, int lane) {
@@ -143,51 +178,58 @@ __device__ __forceinline__ int2 evict_scan(EvictScan* sc, int2 count, int warp, 
 // kKeys: keys that a thread holds; kRest: a run may be longer than that.
 template <int kKeys, bool kRest>
 __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictArgs a) {
-  __shared__ __align__(8) int hist[3][kEvictBins];   // one per pass: no barrier to reuse it
+  __shared__ __align__(16) int hist[3][kEvictBins];   // one per pass: no barrier to reuse it
   __shared__ EvictScan scan_eq, scan_out;
-  __shared__ int warp_sums[32];
-  __shared__ int digit_sh, below_sh, here_sh, max_sh;
+  __shared__ int coarse[3][32];                      // sums of a warp's 64 bins
+  __shared__ int4 lists[32][32];                     // per warp: what its groups list
+  __shared__ int4 pick_sh;                           // digit, keys below it, keys with it, sum
+  __shared__ int max_sh;
   const uint32_t n = cluster_nctas(), rank = cluster_ctarank();
   const int b = blockIdx.x / n;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
+  const int lane = threadIdx.x & 31;
   pdl_launch();
   const int L = a.seq_lens[b];
+  const int cut = a.budget[b];
+  for (int i = threadIdx.x; i < 3 * kEvictBins / 4; i += kEvictThreads)
+    reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
+  if (threadIdx.x == 0) max_sh = -1;
   const bool bad = L < 0 || L > a.max_tokens || L > a.stride;
   const float* w = a.weights + b * a.stride;
   const int32_t* sp = a.slot_pos != nullptr ? a.slot_pos + b * a.stride : nullptr;
   const int Lc = bad ? 0 : L;
-  const int over = max(Lc - max(a.budget[b], 0), 0);     // slots above the budget
+  const int over = max(Lc - max(cut, 0), 0);     // slots above the budget
   // this warp's run of slots: a multiple of 32 for every warp
   const int run = ((Lc + (int)n * kEvictThreads - 1) / ((int)n * kEvictThreads)) * 32;
   const int s0 = min(Lc, ((int)rank * 32 + warp) * run), s1 = min(Lc, s0 + run);
   const int groups = (s1 - s0 + 31) / 32;                // of 32 slots
 
-  // keys of this thread's slots s0 + 32 i + lane, and bit i of `free_bits`
-  // where that slot is free
+  // keys of this thread's slots s0 + 32 i + lane
   uint32_t key[kKeys];
-  uint32_t free_bits = 0, minus_bits = 0;      // minus_bits: -0, whose key is that of 0
   int last = Lc - 1 - a.n_recent;        // free positions: [n_sink, last]
-  auto free_at = [&](int t) {
-    const int p = sp != nullptr ? sp[t] : t;
-    return p >= a.n_sink && p <= last;
+  auto key_of = [&](float x, int p) {
+    return p >= a.n_sink && p <= last ? evict_key(x) : kEvictKept;
   };
-  // f(i, key, free) over this thread's groups; key and free of a slot past the
-  // run are 0 and false
+  // f(i, key) over this thread's groups
   auto each = [&](auto f) {
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
-      if (i < groups) f(i, key[i], (free_bits >> i & 1) != 0);
+      if (i < groups) f(i, key[i]);
     for (int i = kKeys; kRest && i < groups; ++i) {
       const int t = s0 + 32 * i + lane;
-      f(i, t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t));
+      f(i, t < s1 ? key_of(w[t], sp != nullptr ? sp[t] : t) : kEvictKept);
     }
   };
+  // Weight and position of a slot that stays.  A vacated slot before the new
+  // end may be written too: the move fills it.
+  float* nw = a.new_weights != a.weights ? a.new_weights + b * a.stride : nullptr;
+  int32_t* np = a.new_pos != nullptr && a.new_pos != a.slot_pos ? a.new_pos + b * a.stride : nullptr;
+  int copied = s0;                       // this warp's slots before it are written
 
   int n_out = 0, need = 0, n_hole = 0;
   uint32_t kth = 0;       // key of the last slot to leave; `need` slots with it leave
+  bool all_leave = false; // all slots up to kth leave
   if (over > 0) {
-    for (int i = threadIdx.x; i < 3 * kEvictBins; i += kEvictThreads) (&hist[0][0])[i] = 0;
-    if (threadIdx.x == 0) max_sh = -1;
     int mx = -1;
     // all loads first (a slot past the run reads the run's last one), so that
     // they are in flight together
@@ -205,12 +247,15 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     }
 #pragma unroll
     for (int i = 0; i < kKeys; ++i) {
-      const bool in = s0 + 32 * i + lane < s1;
-      minus_bits |= (uint32_t)(key[i] == 0x80000000u) << i;
-      key[i] = in ? evict_key(__uint_as_float(key[i])) : 0u;
-      pos[i] = in ? pos[i] : -1;
-      mx = max(mx, pos[i]);
+      const int t = s0 + 32 * i + lane;
+      if (t < s1) mx = max(mx, pos[i]);
+      // the new end lies at Lc - over or behind it
+      if (t < min(s1, Lc - over)) {
+        if (nw != nullptr) nw[t] = __uint_as_float(key[i]);
+        if (np != nullptr) np[t] = pos[i];
+      }
     }
+    copied = max(s0, min(Lc - over, s0 + 32 * kKeys));
     if (kRest && sp != nullptr)
       for (int t = s0 + 32 * kKeys + lane; t < s1; t += 32) mx = max(mx, sp[t]);
     __syncthreads();
@@ -225,7 +270,7 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     }
 #pragma unroll
     for (int i = 0; i < kKeys; ++i)
-      if (pos[i] >= a.n_sink && pos[i] <= last) free_bits |= 1u << i;
+      key[i] = s0 + 32 * i + lane < s1 ? key_of(__uint_as_float(key[i]), pos[i]) : kEvictKept;
 
     // ---- the n_out-th smallest key, digit by digit ----
 #pragma unroll
@@ -233,107 +278,70 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 0x3FFu : 0x7FFu;
       const uint32_t known = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
-      each([&](int, uint32_t k, bool fr) {
-        if (fr && (k & known) == kth) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
+      each([&](int, uint32_t k) {
+        if (k != kEvictKept && (k & known) == kth) atomicAdd(&hist[pass][(k >> shift) & mask], 1);
       });
+      __syncthreads();
+      {
+        const int2 c = reinterpret_cast<const int2*>(hist[pass])[threadIdx.x];
+        const int sum = __reduce_add_sync(0xffffffffu, c.x + c.y);
+        if (lane == 0) coarse[pass][warp] = sum;
+      }
       if (n > 1) cluster_sync(); else __syncthreads();
-      // thread i owns bins 2i, 2i + 1
-      int c0 = 0, c1 = 0;
-      const uint32_t cell = smem_u32(&hist[pass][2 * threadIdx.x]);
-      if (n == 1) {
-        c0 = hist[pass][2 * threadIdx.x];
-        c1 = hist[pass][2 * threadIdx.x + 1];
-      } else {
-        int2 v[kEvictMaxCluster];
-        ld_cluster_all(cell, n, v);
-#pragma unroll
-        for (uint32_t r = 0; r < kEvictMaxCluster; ++r) {
-          c0 += v[r].x;
-          c1 += v[r].y;
+      if (warp == 0) {
+        // the 64 bins that hold the rank, then the bin
+        const int c = cluster_sum(&coarse[pass][lane], n);
+        const int inc = warp_inclusive(c, lane), all = __shfl_sync(0xffffffffu, inc, 31);
+        const int want = pass == 0 ? min(over, all) : need;
+        if (want > 0) {
+          const int g = __ffs(__ballot_sync(0xffffffffu, inc >= want)) - 1;
+          const int front = __shfl_sync(0xffffffffu, inc - c, g);
+          const int2 v = cluster_sum(reinterpret_cast<const int2*>(&hist[pass][64 * g]) + lane, n);
+          const int before = front + warp_inclusive(v.x + v.y, lane) - v.x - v.y;
+          if (before < want && want <= before + v.x + v.y) {
+            const bool second = want > before + v.x;
+            pick_sh = make_int4(64 * g + 2 * lane + (second ? 1 : 0),
+                                before + (second ? v.x : 0), second ? v.y : v.x, all);
+          }
+        } else if (lane == 0) {
+          pick_sh = make_int4(0, 0, 0, all);
         }
       }
-      const int inc = warp_inclusive(c0 + c1, lane);
-      if (lane == 31) warp_sums[warp] = inc;
       __syncthreads();
-      const int ws = warp_sums[lane];
-      const int wi = warp_inclusive(ws, lane);
+      const int4 pick = pick_sh;
       if (pass == 0) {
-        n_out = min(over, __shfl_sync(0xffffffffu, wi, 31));   // the sum: every free slot
+        n_out = min(over, pick.w);        // the sum: every free slot
         need = n_out;
       }
-      const int before = __shfl_sync(0xffffffffu, wi - ws, warp) + inc - c0 - c1;
-      if (before < need && need <= before + c0 + c1) {
-        const bool second = need > before + c0;
-        digit_sh = 2 * threadIdx.x + (second ? 1 : 0);
-        below_sh = before + (second ? c0 : 0);
-        here_sh = second ? c1 : c0;
-      }
-      __syncthreads();
       if (n_out == 0) break;              // (uniform: nothing is free)
-      kth |= (uint32_t)digit_sh << shift;
-      need -= below_sh;
+      kth |= (uint32_t)pick.x << shift;
+      need -= pick.y;
+      all_leave = need == pick.z;
+      if (all_leave) {                    // uniform: every key with these digits leaves
+        kth = min(kth | ((1u << shift) - 1), kEvictKept - 1);
+        break;
+      }
     }
   }
   const int new_len = Lc - n_out;
-  // weight and position of a slot that stays
-  float* nw = a.new_weights != a.weights ? a.new_weights + b * a.stride : nullptr;
-  int32_t* np = a.new_pos != nullptr && a.new_pos != a.slot_pos ? a.new_pos + b * a.stride : nullptr;
-  auto keep_slot = [&](int t) {
-    if (nw != nullptr) nw[t] = w[t];
-    if (np != nullptr) np[t] = sp != nullptr ? sp[t] : t;
-  };
-  // those of all slots with a bit in `stay`: the weight is its key again, but
-  // for a NaN
-  auto keep_slots = [&](uint32_t stay) {
-    if (np != nullptr) {
-#pragma unroll
-      for (int i0 = 0; i0 < kKeys; i0 += 4) {
-        if (i0 >= groups) break;
-        int p[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int t = min(s0 + 32 * (i0 + i) + lane, s1 - 1);
-          p[i] = sp != nullptr ? sp[t] : t;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-          if (stay >> (i0 + i) & 1) np[s0 + 32 * (i0 + i) + lane] = p[i];
-      }
-    }
-    if (nw != nullptr) {
-#pragma unroll
-      for (int i = 0; i < kKeys; ++i) {
-        if (i >= groups) break;
-        if (stay >> i & 1) {
-          const int t = s0 + 32 * i + lane;
-          const uint32_t u = key[i] ^ ((key[i] >> 31) ? 0x80000000u : 0xFFFFFFFFu);
-          nw[t] = key[i] == 0xFFFFFFFFu ? w[t]
-                                        : __uint_as_float(u | ((minus_bits >> i & 1) << 31));
-        }
-      }
-    }
-  };
   const uint32_t lower = (1u << lane) - 1;
   if (n_out > 0) {
     // ---- ranks of the equal keys, where some of them stay ----
-    const bool all_equal = need == here_sh;
     int eq0 = 0;
-    if (!all_equal) {
+    if (!all_leave) {
       int c = 0;
-      each([&](int, uint32_t k, bool fr) {
-        c += __popc(__ballot_sync(0xffffffffu, fr && k == kth));
-      });
+      each([&](int, uint32_t k) { c += __popc(__ballot_sync(0xffffffffu, k == kth)); });
       int2 sum;
       eq0 = evict_scan(&scan_eq, make_int2(c, 0), warp, lane, rank, n, &sum).x;
     }
-    // the slots of group i that leave, as a mask of lanes; eq counts the
+    // the slots of a group that leave, as a mask of lanes; eq counts the
     // equal keys of the groups before it
-    auto leaving = [&](uint32_t k, bool fr, int& eq) {
-      if (all_equal) return __ballot_sync(0xffffffffu, fr && k <= kth);
-      const uint32_t e = __ballot_sync(0xffffffffu, fr && k == kth);
+    auto leaving = [&](uint32_t k, int& eq) {
+      if (all_leave) return __ballot_sync(0xffffffffu, k <= kth);
+      const uint32_t e = __ballot_sync(0xffffffffu, k == kth);
       const int r = eq + __popc(e & lower);
       eq += __popc(e);
-      return __ballot_sync(0xffffffffu, fr && (k < kth || (k == kth && r < need)));
+      return __ballot_sync(0xffffffffu, k < kth || (k == kth && r < need));
     };
     // slots of group i before the new end, and slots of the run, as masks of
     // lanes
@@ -351,14 +359,14 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
 #pragma unroll
         for (int i = 0; i < kKeys; ++i)
           if (i < groups) {
-            const uint32_t out = leaving(key[i], (free_bits >> i & 1) != 0, eq);
+            const uint32_t out = leaving(key[i], eq);
             mine = lane == i ? out : mine;
           }
       }
       for (int i = max(i0, kKeys); kRest && i < min(groups, i0 + 32); ++i) {
         const int t = s0 + 32 * i + lane;
         const uint32_t out =
-            leaving(t < s1 ? evict_key(w[t]) : 0u, t < s1 && free_at(t), eq);
+            leaving(t < s1 ? key_of(w[t], sp != nullptr ? sp[t] : t) : kEvictKept, eq);
         mine = lane == i - i0 ? out : mine;
       }
       return mine;
@@ -380,40 +388,39 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     c.y = __reduce_add_sync(0xffffffffu, c.y);
     int2 sum, at = evict_scan(&scan_out, c, warp, lane, rank, n, &sum);
     n_hole = sum.x;
-    int2* pairs = a.pairs + b * a.stride;
+    int32_t* holes = a.pairs + 2 * b * a.stride;
     eq = eq_first;
-    uint32_t stay = 0;          // bit i: slot i of this thread stays where it is
     for (int i0 = 0; i0 < groups; i0 += 32) {
       const uint32_t out = i0 == 0 ? first_masks : masks(i0, eq), front = front_of(i0 + lane);
       const uint32_t in = i0 + lane < groups ? run_of(i0 + lane) : 0u;
-      const uint32_t hole = out & front, move = in & ~out & ~front, here = in & ~out & front;
-      const int ih = warp_inclusive(__popc(hole), lane), im = warp_inclusive(__popc(move), lane);
-      const int oh = at.x + ih - __popc(hole), om = at.y + im - __popc(move);
-      const int end = min(32, groups - i0);
-      for (int i = 0; i < end; ++i) {
+      const uint32_t hole = out & front, move = in & ~out & ~front;
+      const int nh = __popc(hole), nm = __popc(move);
+      const int ih = warp_inclusive(nh, lane), im = warp_inclusive(nm, lane);
+      // A slot before the new end is listed as vacated, one behind it as
+      // moving; in the group that the end cuts, vacated slots come first.
+      __syncwarp();
+      lists[warp][lane] = make_int4((int)(hole | move), at.x + ih - nh, at.y + im - nm - nh, 0);
+      __syncwarp();
+      auto list = [&](int i) {
+        const int4 g = lists[warp][i];
         const int t = s0 + 32 * (i0 + i) + lane;
-        const uint32_t h = __shfl_sync(0xffffffffu, hole, i);
-        const uint32_t m = __shfl_sync(0xffffffffu, move, i);
-        if (h != 0) {
-          const int o = __shfl_sync(0xffffffffu, oh, i);
-          if (h >> lane & 1) pairs[o + __popc(h & lower)].x = t;
-        }
-        if (m != 0) {
-          const int o = __shfl_sync(0xffffffffu, om, i);
-          if (m >> lane & 1) pairs[o + __popc(m & lower)].y = t;
-        }
-        const bool stays = __shfl_sync(0xffffffffu, here, i) >> lane & 1;
-        if (i0 + i < kKeys)
-          stay |= (uint32_t)stays << i;
-        else if (stays)
-          keep_slot(t);
+        const bool behind = t >= new_len;
+        if ((uint32_t)g.x >> lane & 1)
+          (behind ? holes + a.stride : holes)[(behind ? g.z : g.y) + __popc((uint32_t)g.x & lower)] = t;
+      };
+      if (i0 == 0) {
+#pragma unroll
+        for (int i = 0; i < kKeys; ++i)
+          if (i < groups) list(i);
       }
+      for (int i = i0 == 0 ? kKeys : 0; kRest && i < min(32, groups - i0); ++i) list(i);
       at.x += __shfl_sync(0xffffffffu, ih, 31);
       at.y += __shfl_sync(0xffffffffu, im, 31);
     }
-    keep_slots(stay);
-  } else {
-    for (int t = s0 + lane; t < s1; t += 32) keep_slot(t);
+  }
+  for (int t = copied + lane; t < min(new_len, s1); t += 32) {
+    if (nw != nullptr) nw[t] = w[t];
+    if (np != nullptr) np[t] = sp != nullptr ? sp[t] : t;
   }
   // every block of the cluster has read seq_lens[b] and its peers' shared
   // memory: the length may be overwritten, and the blocks may end
@@ -432,7 +439,7 @@ template <typename U>
 __global__ void __launch_bounds__(256) evict_move_kernel(
     U* pool, int units, int n_pages, int page_size, const int32_t* page_table, int max_pages,
     const float* weights, const int32_t* slot_pos, float* new_weights, int32_t* new_pos,
-    const int2* pairs, const int32_t* n_pairs, int B, long long stride) {
+    const int32_t* pairs, const int32_t* n_pairs, int B, long long stride) {
   __shared__ long long before[kEvictGroups + 1];   // pairs before each group of sequences
   __shared__ long long sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -514,7 +521,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(
         n = n_pairs[++b];
       }
       bb[q] = b;
-      p[q] = pairs[b * stride + i];
+      p[q] = make_int2(pairs[2 * b * stride + i], pairs[(2 * b + 1) * stride + i]);
       const int32_t* pages = page_table + (long long)b * max_pages;
       const int pt = pages[p[q].x / page_size], pf = pages[p[q].y / page_size];
       if (pt < 0 || pt >= n_pages || pf < 0 || pf >= n_pages) {
