@@ -994,17 +994,17 @@ mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, 
                              (T + kNormThreads / 32 - 1) / (kNormThreads / 32);
     if (blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
     if (dims->dtype == MLA_F32)
-      norm_rope_kernel<float><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+      launch_pdl(norm_rope_kernel<float>, dim3((unsigned)blocks), kNormThreads, 0, st, a);
     else
-      norm_rope_kernel<__nv_bfloat16><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+      launch_pdl(norm_rope_kernel<__nv_bfloat16>, dim3((unsigned)blocks), kNormThreads, 0, st, a);
     return check_launch();
   }
   const long long blocks = ((long long)T * (H + 2) + kNormThreads / 32 - 1) / (kNormThreads / 32);
   if (blocks > 0x7FFFFFFFll) return MLA_ERR_UNSUPPORTED;
   if (dims->dtype == MLA_F32)
-    norm_rope_any_kernel<float><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+    launch_pdl(norm_rope_any_kernel<float>, dim3((unsigned)blocks), kNormThreads, 0, st, a);
   else
-    norm_rope_any_kernel<__nv_bfloat16><<<(unsigned)blocks, kNormThreads, 0, st>>>(a);
+    launch_pdl(norm_rope_any_kernel<__nv_bfloat16>, dim3((unsigned)blocks), kNormThreads, 0, st, a);
   return check_launch();
 }
 
@@ -1061,13 +1061,15 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   cfg.gridDim = dim3((unsigned)(B * cluster));
   cfg.blockDim = dim3(kEvictThreads);
   cfg.stream = st;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
   at[0].val.clusterDim.x = (unsigned)cluster;
   at[0].val.clusterDim.y = 1;
   at[0].val.clusterDim.z = 1;
+  at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[1].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = 2;
   auto plan = stride <= kFew * cluster ? evict_plan_kernel<kEvictFewKeys, false>
                                        : evict_plan_kernel<kEvictKeys, true>;
   if (cudaLaunchKernelEx(&cfg, plan, a) != cudaSuccess) return MLA_ERR_CUDA;
@@ -1077,27 +1079,20 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
                                              (dims->dtype == MLA_F32 ? 4 : 2);
   // one wave (four blocks per SM), no more warps than there can be pairs; may
   // start while the plan runs
-  cudaLaunchConfig_t mv{};
-  mv.gridDim = dim3((unsigned)std::min<long long>(4LL * sm_count(),
-                                                  ((long long)B * stride / 2 + 7) / 8 + 1));
-  mv.blockDim = dim3(256);
-  mv.stream = st;
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  mv.attrs = at;
-  mv.numAttrs = 1;
+  const dim3 grid((unsigned)std::min<long long>(4LL * sm_count(),
+                                                ((long long)B * stride / 2 + 7) / 8 + 1));
   const int32_t* pairs = a.pairs;
   const int32_t* n_pairs = a.n_pairs;
   const cudaError_t moved =
       row_bytes % 16 == 0 && aligned16(pool)
-          ? cudaLaunchKernelEx(&mv, evict_move_kernel<uint4>, static_cast<uint4*>(pool),
-                               (int)(row_bytes / 16), n_pages, dims->page_size, page_table,
-                               max_pages, weights, slot_pos, new_weights, new_pos, pairs, n_pairs,
-                               B, (long long)stride)
-          : cudaLaunchKernelEx(&mv, evict_move_kernel<uint16_t>, static_cast<uint16_t*>(pool),
-                               (int)(row_bytes / 2), n_pages, dims->page_size, page_table,
-                               max_pages, weights, slot_pos, new_weights, new_pos, pairs, n_pairs,
-                               B, (long long)stride);
+          ? launch_pdl(evict_move_kernel<uint4>, grid, 256, 0, st, static_cast<uint4*>(pool),
+                       (int)(row_bytes / 16), n_pages, dims->page_size, page_table, max_pages,
+                       weights, slot_pos, new_weights, new_pos, pairs, n_pairs, B,
+                       (long long)stride)
+          : launch_pdl(evict_move_kernel<uint16_t>, grid, 256, 0, st,
+                       static_cast<uint16_t*>(pool), (int)(row_bytes / 2), n_pages,
+                       dims->page_size, page_table, max_pages, weights, slot_pos, new_weights,
+                       new_pos, pairs, n_pairs, B, (long long)stride);
   if (moved != cudaSuccess) return MLA_ERR_CUDA;
   return check_launch();
 }

@@ -102,6 +102,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t*
   __shared__ int start_sh[kPlanSeqs];  // start, where it fits
   __shared__ int aligned;              // t of the aligned split, or 0
   __shared__ int first_sh[kPlanSeqs + 1];
+  pdl_wait();
   pdl_launch();
   int32_t* first = B <= kPlanSeqs ? first_sh : first_global;
   for (int k = threadIdx.x; k < G; k += kPlanThreads) cuts[k].v = -1;
@@ -254,6 +255,7 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse,
                                                             int H, __nv_bfloat16* o, float* lse) {
   __shared__ float4 part[8][128];
   pdl_wait();
+  pdl_launch();
   const ChunkCut c = cuts[blockIdx.x];
   if (c.v < 0) return;
   const int n = c.k1 - c.k0 + 1;
@@ -361,10 +363,10 @@ inline mla_status launch_chunk_tc_impl(
   if (cudaFuncSetAttribute(decode_tc_kernel<true>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                            (int)kSmemBytes) != cudaSuccess)
     return MLA_ERR_CUDA;
-  chunk_plan_kernel<<<1, kPlanThreads, 0, st>>>(cu_q, seq_lens, B, H, total_q, max_q, max_pages * kPage,
-                                        (int)c.V, c.G, first, vseq, start, cuts,
-                                        worker_v, lo);
-  if (cudaGetLastError() != cudaSuccess) return MLA_ERR_CUDA;
+  if (launch_pdl(chunk_plan_kernel, dim3(1), kPlanThreads, 0, st, cu_q, seq_lens, B, H, total_q,
+                 max_q, max_pages * kPage, (int)c.V, c.G, first, vseq, start, cuts, worker_v,
+                 lo) != cudaSuccess)
+    return MLA_ERR_CUDA;
   DecodeTcParams p{};
   p.pool = static_cast<const uint8_t*>(pool);
   p.page_table = page_table;
@@ -384,25 +386,10 @@ inline mla_status launch_chunk_tc_impl(
   p.V = (int)c.V;
   p.o = o;
   p.lse = lse;
-  // both may start while their predecessor runs: the attention sets up its
-  // barriers and TMEM under the plan
-  cudaLaunchAttribute pdl[1];
-  pdl[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  pdl[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(2 * c.G);
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = kSmemBytes;
-  cfg.stream = st;
-  cfg.attrs = pdl;
-  cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, decode_tc_kernel<true>, tQ, tQK, tPV, p) != cudaSuccess)
-    return MLA_ERR_CUDA;
-  cfg.gridDim = dim3(c.G, 16);
-  cfg.blockDim = dim3(256);
-  cfg.dynamicSmemBytes = 0;
-  if (cudaLaunchKernelEx(&cfg, chunk_combine_kernel, (const float*)ws_lse, (const float*)ws_o,
-                         (const ChunkCut*)cuts, (const VSeq*)vseq, H, o, lse) != cudaSuccess)
+  if (launch_pdl(decode_tc_kernel<true>, dim3(2 * c.G), kThreads, kSmemBytes, st, tQ, tQK, tPV,
+                 p) != cudaSuccess ||
+      launch_pdl(chunk_combine_kernel, dim3(c.G, 16), 256, 0, st, ws_lse, ws_o, cuts, vseq, H, o,
+                 lse) != cudaSuccess)
     return MLA_ERR_CUDA;
   return MLA_OK;
 }

@@ -188,12 +188,13 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   const int b = blockIdx.x / n;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
   const int lane = threadIdx.x & 31;
-  pdl_launch();
-  const int L = a.seq_lens[b];
-  const int cut = a.budget[b];
   for (int i = threadIdx.x; i < 3 * kEvictBins / 4; i += kEvictThreads)
     reinterpret_cast<int4*>(hist)[i] = make_int4(0, 0, 0, 0);
   if (threadIdx.x == 0) max_sh = -1;
+  pdl_wait();
+  pdl_launch();
+  const int L = a.seq_lens[b];
+  const int cut = a.budget[b];
   const bool bad = L < 0 || L > a.max_tokens || L > a.stride;
   const float* w = a.weights + b * a.stride;
   const int32_t* sp = a.slot_pos != nullptr ? a.slot_pos + b * a.stride : nullptr;
@@ -444,6 +445,7 @@ __global__ void __launch_bounds__(256) evict_move_kernel(
   __shared__ long long sums[8];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   pdl_wait();
+  pdl_launch();
   const long long warps = (long long)gridDim.x * 8, me = (long long)blockIdx.x * 8 + warp;
   long long lo, hi;          // this warp's pairs
   int b, i, n;               // sequence of pair lo, the pair within it, its pairs

@@ -117,6 +117,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_kernel(const __grid_co
   constexpr int dqk = kNormDN + kNormDR, D = kNormDC + kNormDR;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int groups = (a.H + kNormHeads - 1) / kNormHeads;
+  pdl_wait();
+  pdl_launch();
   const long long q_blocks = (long long)a.T * groups;
   if ((long long)blockIdx.x < q_blocks) {
     // ---------------- query heads ----------------
@@ -251,6 +253,8 @@ __global__ void __launch_bounds__(kNormThreads) norm_rope_any_kernel(const __gri
   const long long i = (long long)blockIdx.x * (kNormThreads / 32) + (threadIdx.x >> 5);
   const long long t = i / (a.H + 2);
   const int h = (int)(i % (a.H + 2));
+  pdl_wait();
+  pdl_launch();
   if (t >= a.T) return;
   const int dqk = a.d_nope + a.d_rope, D = a.d_latent + a.d_rope;
   const T* row = static_cast<const T*>(a.y) + t * a.ys_tok;

@@ -154,6 +154,9 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
     tmem_relinquish<2>();
   }
 
+  pdl_wait();
+  pdl_launch();
+
   // ---- this pair's run: first sequence, first tile, cost at its end ----
   constexpr int kOpen = kQStat ? kOpenPages : 0;
   bool wrong = false;
@@ -600,8 +603,9 @@ inline mla_status launch_weights(bool (*make_tmap)(CUtensorMap*, const void*, in
   if (cudaFuncSetAttribute(kfn, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) !=
       cudaSuccess)
     return MLA_ERR_CUDA;
-  kfn<<<2 * pairs, kThreads, smem, st>>>(tQ, tK, p);
-  return cudaGetLastError() == cudaSuccess ? MLA_OK : MLA_ERR_CUDA;
+  return launch_pdl(kfn, dim3(2 * pairs), kThreads, smem, st, tQ, tK, p) == cudaSuccess
+             ? MLA_OK
+             : MLA_ERR_CUDA;
 }
 
 }  // namespace mla
