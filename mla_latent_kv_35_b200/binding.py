@@ -68,8 +68,8 @@ class MLADims:
                     self.rope_base, MLA_BF16 if self.dtype == "bf16" else MLA_F32)
 
     def __getstate__(self):
-        """Copies and pickles leave the cached C struct behind (_ref)."""
-        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+        """Copies and pickles leave the cached C struct behind (_c)."""
+        return {k: v for k, v in self.__dict__.items() if k != "_c"}
 
     @property
     def torch_dtype(self):
@@ -82,7 +82,7 @@ class MLADims:
                        w.page_size, w.scale, w.rope_base, w.dtype)
 
 
-_lib = None
+_lib = _pycall = None
 
 _P, _I, _Z = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
 _SIGS = {
@@ -151,8 +151,23 @@ def lib():
             f = getattr(h, name)
             f.argtypes = args
             f.restype = res
+        _bind(h)
         _lib = h
     return _lib
+
+
+def _bind(h):
+    """Point the native calls at the functions of library handle h."""
+    global _pycall
+    try:
+        from . import _pycall as m
+    except ImportError as e:
+        raise ImportError("the Python calls are missing: build them with "
+                          "`python -m mla_latent_kv_35_b200.build`") from e
+    m.bind(*(ctypes.cast(getattr(h, f), _P).value for f in (
+        "mla_chunk_attention", "mla_attn_weights", "mla_out_proj_bf16", "mla_norm_rope",
+        "mla_cache_evict")))
+    _pycall = m
 
 
 def _ptr(t):
@@ -174,42 +189,28 @@ def _dev(*ts):
             raise ValueError("tensors must live on the CUDA device")
 
 
-def _ref(dims: MLADims):
-    """The dims struct by reference, built once per MLADims."""
-    c = dims.__dict__.get("_ref")
+def _addr(dims: MLADims) -> int:
+    """Address of the dims struct, built once per MLADims."""
+    c = dims.__dict__.get("_c")
     if c is None:
-        c = ctypes.byref(dims.c())
-        object.__setattr__(dims, "_ref", c)
-    return c
+        s = dims.c()
+        c = (ctypes.addressof(s), s)
+        object.__setattr__(dims, "_c", c)
+    return c[0]
 
 
-def _here(dev: int, what: str, t, dtype, numel: int) -> int:
-    """Address of a tensor that must be on the current device `dev`, contiguous, of `dtype` and
-    at least `numel` elements."""
-    if (t.dtype is dtype and t.get_device() == dev and t.numel() >= numel
-            and t.is_contiguous()):
-        return t.data_ptr()
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: the tensor must live on the current CUDA device")
-    if t.dtype is not dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    raise ValueError(f"{what}: expected a contiguous tensor of at least {numel} elements")
+def _native():
+    """The checks and calls of the operators around the cache (csrc/pycall.cpp), bound to lib():
+    tensors on the current device, contiguous, of the right type and large enough, or ValueError."""
+    if _lib is None:
+        lib()
+    return _pycall
 
 
-def _rows(dev: int, what: str, t, dtype, rows: int, width: int, stride: int) -> int:
-    """Address of `rows` rows of `width` elements, `stride` apart, on the current device; the
-    tensor is a view of them whose storage holds them all."""
-    if (t.dtype is dtype and t.get_device() == dev and stride >= width
-            and t.numel() >= rows * stride and t.is_contiguous()):
-        return t.data_ptr()
-    if t.get_device() != dev:
-        raise ValueError(f"{what}: the tensor must live on the current CUDA device")
-    if t.dtype is not dtype:
-        raise ValueError(f"{what}: expected {dtype}, got {t.dtype}")
-    need = (t.storage_offset() + (rows - 1) * stride + width) * t.element_size() if rows > 0 else 0
-    if stride < width or t.untyped_storage().nbytes() < need:
-        raise ValueError(f"{what}: the tensor does not hold {rows} rows of {width} at stride {stride}")
-    return t.data_ptr()
+def _where():
+    """The current device and its current stream, as _native()'s functions take them."""
+    dev = torch.cuda.current_device()
+    return dev, torch._C._cuda_getCurrentRawStream(dev)
 
 
 # --------------------------------------------------------------------------
@@ -363,7 +364,7 @@ def mla_out_proj(dims: MLADims, o_lat, w_uv, w_o, scratch, out, T: int):
 
 
 def mla_chunk_attention_workspace_size(dims: MLADims, B: int, total_q: int, max_q: int) -> int:
-    return int(lib().mla_chunk_attention_workspace_size(_ref(dims), B, total_q, max_q))
+    return int(lib().mla_chunk_attention_workspace_size(dims.c(), B, total_q, max_q))
 
 
 def mla_chunk_attention(dims: MLADims, qbuf, cu_q, total_q, max_q, pool, n_pages, page_table,
@@ -371,19 +372,9 @@ def mla_chunk_attention(dims: MLADims, qbuf, cu_q, total_q, max_q, pool, n_pages
     """Attention of ragged chunks of new tokens over the paged cache: sequence b's queries are
     tokens cu_q[b] .. cu_q[b + 1] - 1 of qbuf and the last of its seq_lens[b] cached tokens
     (include/mla.h).  o_lat bf16, lse fp32."""
-    dev = torch.cuda.current_device()
-    dt, i32 = dims.torch_dtype, torch.int32
-    H, D = dims.n_heads, dims.d_latent + dims.d_rope
-    _check("mla_chunk_attention", lib().mla_chunk_attention(
-        _ref(dims), _here(dev, "qbuf", qbuf, dt, total_q * H * D),
-        _here(dev, "cu_q", cu_q, i32, B + 1), total_q, max_q,
-        _here(dev, "pool", pool, dt, n_pages * dims.page_size * D), n_pages,
-        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-        _here(dev, "seq_lens", seq_lens, i32, B), B,
-        _here(dev, "workspace", workspace, torch.uint8, 0), workspace.numel(),
-        _here(dev, "o_lat", o_lat, dt, total_q * H * dims.d_latent),
-        _here(dev, "lse", lse, torch.float32, total_q * H),
-        torch._C._cuda_getCurrentRawStream(dev)))
+    _check("mla_chunk_attention", _native().chunk_attention(
+        _addr(dims), *_where(), qbuf, cu_q, total_q, max_q, pool, n_pages, page_table, max_pages,
+        seq_lens, B, workspace, o_lat, lse))
 
 
 def mla_attn_weights(dims: MLADims, qbuf, lse, cu_q, total_q, max_q, pool, n_pages, page_table,
@@ -391,35 +382,19 @@ def mla_attn_weights(dims: MLADims, qbuf, lse, cu_q, total_q, max_q, pool, n_pag
     """Attention weight that the cached tokens receive from a chunk's queries, added to keep times
     what they had gathered before it (w_in, or None); lse as mla_decode or mla_chunk_attention
     returned it (include/mla.h)."""
-    dev = torch.cuda.current_device()
-    dt, i32, f32 = dims.torch_dtype, torch.int32, torch.float32
-    H, D = dims.n_heads, dims.d_latent + dims.d_rope
-    _check("mla_attn_weights", lib().mla_attn_weights(
-        _ref(dims), _here(dev, "qbuf", qbuf, dt, total_q * H * D),
-        _here(dev, "lse", lse, f32, total_q * H), _here(dev, "cu_q", cu_q, i32, B + 1), total_q,
-        max_q, _here(dev, "pool", pool, dt, n_pages * dims.page_size * D), n_pages,
-        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-        _here(dev, "seq_lens", seq_lens, i32, B), B,
-        None if w_in is None else _here(dev, "w_in", w_in, f32, B * stride), keep,
-        _here(dev, "w_out", w_out, f32, B * stride), stride,
-        torch._C._cuda_getCurrentRawStream(dev)))
+    _check("mla_attn_weights", _native().attn_weights(
+        _addr(dims), *_where(), qbuf, lse, cu_q, total_q, max_q, pool, n_pages, page_table,
+        max_pages, seq_lens, B, w_in, keep, w_out, stride))
 
 
 def mla_out_proj_bf16_scratch_size(dims: MLADims, T: int) -> int:
-    return int(lib().mla_out_proj_bf16_scratch_size(_ref(dims), T))
+    return int(lib().mla_out_proj_bf16_scratch_size(dims.c(), T))
 
 
 def mla_out_proj_bf16(dims: MLADims, o_lat, w_uv, w_o, scratch, out, T: int):
     """mla_out_proj of bf16 rows (mla_chunk_attention's output)."""
-    dev = torch.cuda.current_device()
-    dt, H, hv = dims.torch_dtype, dims.n_heads, dims.n_heads * dims.d_v
-    _check("mla_out_proj_bf16", lib().mla_out_proj_bf16(
-        _ref(dims), _here(dev, "o_lat", o_lat, dt, T * H * dims.d_latent),
-        _here(dev, "w_uv", w_uv, dt, hv * dims.d_latent),
-        _here(dev, "w_o", w_o, dt, dims.d_model * hv),
-        _here(dev, "scratch", scratch, torch.uint8, 0), scratch.numel(),
-        _here(dev, "out", out, torch.float32, T * dims.d_model), T,
-        torch._C._cuda_getCurrentRawStream(dev)))
+    _check("mla_out_proj_bf16", _native().out_proj_bf16(
+        _addr(dims), *_where(), o_lat, w_uv, w_o, scratch, out, T))
 
 
 def mla_norm_rope(dims: MLADims, y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batch_idx, slot,
@@ -428,31 +403,13 @@ def mla_norm_rope(dims: MLADims, y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batc
     """RMS norms of the query heads, the latent and the RoPE key (weights w_q, w_c, w_kr, each or
     None), the rotation by pos and the append at slot, in one pass over the A0 rows y.  pool,
     qbuf and ckr may be None (include/mla.h)."""
-    dev = torch.cuda.current_device()
-    dt, i32 = dims.torch_dtype, torch.int32
-    H, dqk = dims.n_heads, dims.d_nope + dims.d_rope
-    D = dims.d_latent + dims.d_rope
-    bi = sl = pt = pl = None
-    n_seqs = 0
-    if pool is not None:
-        n_seqs = page_table.numel() // max_pages if max_pages > 0 else 0
-        bi, sl = _here(dev, "batch_idx", batch_idx, i32, T), _here(dev, "slot", slot, i32, T)
-        pt = _here(dev, "page_table", page_table, i32, max_pages)
-        pl = _here(dev, "pool", pool, dt, n_pages * dims.page_size * D)
-    _check("mla_norm_rope", lib().mla_norm_rope(
-        _ref(dims), _rows(dev, "y", y, dt, T, H * dqk + D, y_stride_tok), y_stride_tok,
-        None if w_q is None else _here(dev, "w_q", w_q, dt, dqk),
-        None if w_c is None else _here(dev, "w_c", w_c, dt, dims.d_latent),
-        None if w_kr is None else _here(dev, "w_kr", w_kr, dt, dims.d_rope), eps,
-        _here(dev, "pos", pos, i32, T), bi, sl, pt, n_seqs, max_pages, pl, n_pages,
-        _rows(dev, "q", q, dt, T, H * dqk, q_stride_tok), q_stride_tok,
-        None if qbuf is None else _here(dev, "qbuf", qbuf, dt, T * H * D),
-        None if ckr is None else _rows(dev, "ckr", ckr, dt, T, D, ckr_stride_tok), ckr_stride_tok,
-        T, torch._C._cuda_getCurrentRawStream(dev)))
+    _check("mla_norm_rope", _native().norm_rope(
+        _addr(dims), *_where(), y, y_stride_tok, w_q, w_c, w_kr, eps, pos, batch_idx, slot,
+        page_table, max_pages, pool, n_pages, q, q_stride_tok, qbuf, ckr, ckr_stride_tok, T))
 
 
 def mla_cache_evict_workspace_size(dims: MLADims, B: int, stride: int) -> int:
-    return int(lib().mla_cache_evict_workspace_size(_ref(dims), B, stride))
+    return int(lib().mla_cache_evict_workspace_size(dims.c(), B, stride))
 
 
 def mla_cache_evict(dims: MLADims, pool, n_pages, fp8_rows, page_table, max_pages, seq_lens, B,
@@ -461,22 +418,10 @@ def mla_cache_evict(dims: MLADims, pool, n_pages, fp8_rows, page_table, max_page
     """Cut every sequence to its budget: the cached tokens with the least gathered weight leave,
     the first n_sink and the last n_recent positions excepted, and the survivors behind the new
     end move into the vacated slots (include/mla.h).  fp8_rows: pool is the 8-bit cache."""
-    dev = torch.cuda.current_device()
-    i32, f32 = torch.int32, torch.float32
-    row = FP8_ROW_BYTES if fp8_rows else dims.d_latent + dims.d_rope
-    _check("mla_cache_evict", lib().mla_cache_evict(
-        _ref(dims), _here(dev, "pool", pool, torch.uint8 if fp8_rows else dims.torch_dtype,
-                          n_pages * dims.page_size * row), n_pages, 1 if fp8_rows else 0,
-        _here(dev, "page_table", page_table, i32, B * max_pages), max_pages,
-        _here(dev, "seq_lens", seq_lens, i32, B), B,
-        _here(dev, "weights", weights, f32, B * stride),
-        None if slot_pos is None else _here(dev, "slot_pos", slot_pos, i32, B * stride), stride,
-        _here(dev, "budget", budget, i32, B), n_sink, n_recent,
-        _here(dev, "new_weights", new_weights, f32, B * stride),
-        None if new_pos is None else _here(dev, "new_pos", new_pos, i32, B * stride),
-        _here(dev, "new_lens", new_lens, i32, B),
-        _here(dev, "workspace", workspace, torch.uint8, 0), workspace.numel(),
-        torch._C._cuda_getCurrentRawStream(dev)))
+    _check("mla_cache_evict", _native().cache_evict(
+        _addr(dims), *_where(), pool, n_pages, 1 if fp8_rows else 0, page_table, max_pages,
+        seq_lens, B, weights, slot_pos, stride, budget, n_sink, n_recent, new_weights, new_pos,
+        new_lens, workspace, FP8_ROW_BYTES))
 
 
 def mla_get_device_status() -> int:
