@@ -181,8 +181,8 @@ __device__ __forceinline__ bool named_bar_or(int id, int nthreads, bool pred) {
 // Stores a warp's 32 x 32 words (lane = row) as rows of 128 contiguous bytes,
 // `pitch` bytes apart, of which the first `valid` exist.  Eight rows at a time
 // turn around in the warp's 1 KB of shared memory, so that a store instruction
-// covers four whole lines instead of sixteen bytes of 32 (O of a piece: 6.4 ->
-// 1.5 us).
+// covers four whole lines instead of sixteen bytes of 32 (O of a piece: 6.4 to
+// 9 -> 4 us).
 __device__ __forceinline__ void store_rows32(uint32_t sx, const uint32_t (&x)[32], uint8_t* dst,
                                              size_t pitch, int valid, int lane) {
   const int r = lane & 7;
