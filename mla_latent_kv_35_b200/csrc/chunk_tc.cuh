@@ -102,12 +102,16 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t*
   __shared__ int start_sh[kPlanSeqs];  // start, where it fits
   __shared__ int aligned;              // t of the aligned split, or 0
   __shared__ int first_sh[kPlanSeqs + 1];
+  __shared__ int len_sh[kPlanThreads];
   pdl_wait();
   pdl_launch();
   int32_t* first = B <= kPlanSeqs ? first_sh : first_global;
   for (int k = threadIdx.x; k < G; k += kPlanThreads) cuts[k].v = -1;
+  // (lengths of the first sequences come along with cu_q: one trip to memory)
+  const int L_mine = threadIdx.x < B ? seq_lens[threadIdx.x] : 0;
   bool wrong = false;
   for (int b = threadIdx.x; b < B; b += kPlanThreads) wrong |= chunk_bad(cu_q, b, total_q, max_q);
+  len_sh[threadIdx.x] = L_mine;
   if (__syncthreads_or(wrong)) {
     for (int v = threadIdx.x; v <= V; v += kPlanThreads) start[v] = 0;
     for (int k = threadIdx.x; k <= G; k += kPlanThreads) lo[k] = 0;
@@ -137,7 +141,7 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t*
       s.row0 = (v - first[b]) * 128;
       s.q0 = cu_q[b];
       s.T = cu_q[b + 1] - s.q0;
-      s.L = seq_lens[b];
+      s.L = b < kPlanThreads ? len_sh[b] : seq_lens[b];
       if (s.L < s.T || s.L > max_tokens) {
         if (s.row0 == 0) raise_flag(kFlagBounds);
         s.L = 0;
@@ -190,36 +194,31 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t*
         for (int i = 0; i < kMine; ++i) m += (nb[i] + mid - 1) / mid;
         if ((int)__reduce_add_sync(0xffffffffu, m) <= G) z = mid; else a = mid + 1;
       }
-      if (a + kOpen <= (cost + G - 1) / G + 2) {
-        t = a;
-        int m = 0;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) m += (nb[i] + t - 1) / t;
-        int k = m;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const int y = __shfl_up_sync(0xffffffffu, k, o);
-          if (lane >= o) k += y;
-        }
-        const int used = __shfl_sync(0xffffffffu, k, 31);
-        k -= m;
-#pragma unroll
-        for (int i = 0; i < kMine; ++i) {
-          const int v = kMine * lane + i, n = (nb[i] + t - 1) / t;
-          for (int j = 0; j < n; ++j) {
-            lo[k + j] = first_block[v] + (int)((long long)nb[i] * j / n);
-            worker_v[k + j] = v;
-            if (j + 1 < n) cuts[k + j] = ChunkCut{v, k, k + n - 1, 0};
-          }
-          k += n;
-        }
-        for (int j = used + lane; j <= G; j += 32) lo[j] = blocks;
-      }
+      if (a + kOpen <= (cost + G - 1) / G + 2) t = a;
     }
     if (lane == 0) aligned = t;
   }
   __syncthreads();
-  if (aligned > 0) return;
+  // quotients of 64 bits take a third of a microsecond each
+  const bool small = cost < (1 << 24) && G < 255;           // 32 bits hold k cost
+  auto quotient = [&](long long x, long long y) {
+    return small ? (long long)((uint32_t)x / (uint32_t)y) : x / y;
+  };
+  if (aligned > 0) {
+    const int v = threadIdx.x;                   // live <= 128
+    const int v0 = v < live ? first_block[v] : 0;
+    const int nb = v < live ? first_block[v + 1] - v0 : 0;
+    const int n = (nb + aligned - 1) / aligned;
+    int used;
+    const int k = block_exclusive(n, warp_sums, &used);
+    for (int j = 0; j < n; ++j) {
+      lo[k + j] = v0 + (int)quotient((long long)nb * j, n);
+      worker_v[k + j] = v;
+      if (j + 1 < n) cuts[k + j] = ChunkCut{v, k, k + n - 1, 0};
+    }
+    for (int j = used + threadIdx.x; j <= G; j += kPlanThreads) lo[j] = blocks;
+    return;
+  }
   // boundary k lies at floor(k cost / workers): in row block v's part [c0, c1),
   // at its start or kOpen blocks less into it
   const long long workers = min(G, blocks);
@@ -229,8 +228,8 @@ __global__ void __launch_bounds__(kPlanThreads) chunk_plan_kernel(const int32_t*
     const long long c0 = v0 + (long long)kOpen * v;
     const long long c1 = first_block[v + 1] + (long long)kOpen * (v + 1);
     int k0 = -1, k1 = -1;              // first and last worker of a row block that is cut
-    for (long long k = (c0 * workers + cost - 1) / cost; k < workers; ++k) {
-      const long long at = k * cost / workers;
+    for (long long k = quotient(c0 * workers + cost - 1, cost); k < workers; ++k) {
+      const long long at = quotient(k * cost, workers);
       if (at >= c1) break;
       const int x = (int)max(at - c0 - kOpen, 0ll);
       lo[k] = v0 + x;
