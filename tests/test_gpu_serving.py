@@ -341,6 +341,60 @@ def test_a_graph_of_padded_chunks_and_buffers_of_many_lengths():
 
 
 @gpu
+def test_two_layers_on_two_streams_at_once():
+    """Two layers step, gather and evict on streams of their own at the same time, through graphs and
+    eagerly: the same bits as one after the other."""
+    n, qs = 3, [70, 1, 5]
+    T, cu = sum(qs), np.concatenate([[0], np.cumsum(qs)])
+    runs = []
+    for seed in (11, 12):
+        layer, W, rng = make(norms=True, H=16, n_seqs=n, seed=seed)
+        ctx = [200, 64, 129]
+        layer.prefill_from_hidden([q(rng.standard_normal((k, 256)), "bf16") for k in ctx])
+        h, bi, pos, places = tokens(rng, layer, qs, ctx, ctx)
+        lens = i32(np.array(ctx) + qs)
+        state = dict(layer=layer, args=(to_dev(h, "bf16"), i32(bi), i32(pos), i32(cu), T, max(qs)),
+                     pool=layer.pool.clone(), lens=lens, weights=torch.zeros((n, 512), device=DEV),
+                     budget=i32([150, 60, 100]))
+
+        def step(s=state):
+            layer = s["layer"]
+            layer.pool.copy_(s["pool"])
+            layer.seq_lens.copy_(s["lens"])
+            s["weights"].zero_()
+            bf = layer.extend(*s["args"])
+            layer.gather_weights(bf, s["args"][3], T, max(qs), s["weights"])
+            layer.evict(s["weights"], s["budget"], 2, 8)
+            return [bf["out"], bf["lse"], s["weights"], layer.seq_lens, layer.pool]
+        state["step"] = step
+        step()
+        torch.cuda.synchronize()
+        state["ref"] = [t.clone() for t in step()]
+        state["stream"] = torch.cuda.Stream()
+        state["graph"] = torch.cuda.CUDAGraph()
+        torch.cuda.synchronize()
+        with torch.cuda.graph(state["graph"], stream=state["stream"]):
+            state["outs"] = step()
+        runs.append(state)
+    assert status() == 0
+    torch.cuda.synchronize()
+    same = lambda a, b: torch.equal(a.contiguous().view(torch.uint8), b.contiguous().view(torch.uint8))  # noqa: E731
+    for eager in (False, True):
+        for _ in range(20):
+            for s in runs:
+                with torch.cuda.stream(s["stream"]):
+                    if eager:
+                        s["outs"] = s["step"]()
+                    else:
+                        s["graph"].replay()
+        torch.cuda.synchronize()
+        assert status() == 0
+        for s in runs:
+            for a, b in zip(s["outs"], s["ref"]):
+                assert same(a, b)
+
+
+@gpu
 def test_refusals_of_the_layer():
     layer, W, rng = make(kind="fp8")
     with pytest.raises(ValueError):
