@@ -33,14 +33,16 @@
 //     before the new end, and the new length.  Those of a vacated slot are
 //     written too, while they are at hand, since the move overwrites them.
 // evict_move_kernel: every warp takes an even share of all sequences' pairs
-// and copies row, weight and position, two rows in flight.  (A grid of blocks
+// and copies row, weight and position, two rows in flight; pairs and page ids
+// are looked up 32 at a time, a lane each (two rows at a time, three trips to
+// memory for each: 55 against 52 us for the ragged batch).  (A grid of blocks
 // per sequence left the SMs of the short ones idle: 116 us against 33 for 64
 // ragged sequences.)
 //
 // Bound: the plan by latency (loads, then three to six cluster barriers) and by
 // instruction issue (32 warps on one SM), the move by memory bandwidth.
-// Measured in a graph: one token of 16 x 4097 12.9 us (plan 9.5), 64 sequences
-// of 129 to 32769 tokens to 30 % 55 us (plan 18.5), 4 x 131072 halved 78 us
+// Measured in a graph: one token of 16 x 4097 12.3 us (plan 9.5), 64 sequences
+// of 129 to 32769 tokens to 30 % 52 us (plan 18.5), 4 x 131072 halved 76 us
 // (plan 21).
 #pragma once
 
@@ -507,60 +509,62 @@ __global__ void __launch_bounds__(256) evict_move_kernel(
       n = n_pairs[++b];
     }
   }
-  constexpr int kRows = 2;                 // rows in flight
-  for (long long g = lo; g < hi;) {
-    int2 p[kRows];
-    int bb[kRows];
-    U* to[kRows];
-    const U* from[kRows];
-    int live = 0;
-#pragma unroll
-    for (int q = 0; q < kRows; ++q) {
-      to[q] = nullptr;
-      if (g >= hi) continue;
-      while (i >= n) {
-        i = 0;
-        n = n_pairs[++b];
-      }
-      bb[q] = b;
-      p[q] = make_int2(pairs[2 * b * stride + i], pairs[(2 * b + 1) * stride + i]);
-      const int32_t* pages = page_table + (long long)b * max_pages;
-      const int pt = pages[p[q].x / page_size], pf = pages[p[q].y / page_size];
-      if (pt < 0 || pt >= n_pages || pf < 0 || pf >= n_pages) {
-        if (lane == 0) raise_flag(kFlagBounds);
-      } else {
-        to[q] = pool + ((long long)pt * page_size + p[q].x % page_size) * units;
-        from[q] = pool + ((long long)pf * page_size + p[q].y % page_size) * units;
-      }
-      ++live;
-      ++i;
-      ++g;
+  // A lane looks up one pair (slots, pages, rows) and moves its weight and
+  // position; then the warp copies the 32 pairs' rows.
+  constexpr int kRows = 2;                 // rows in flight (3 or 4 leave fewer warps: no faster)
+  for (long long g = lo; g < hi; g += 32) {
+    const int count = (int)min(32ll, hi - g);
+    int lb = b, li = i + min(lane, count - 1), ln = n;     // (a lane past the end: the last pair)
+    while (li >= ln) {
+      li -= ln;
+      ln = n_pairs[++lb];
     }
-    for (int u0 = 0; u0 < units; u0 += 96) {
-      U v[kRows][3];
-#pragma unroll
-      for (int q = 0; q < kRows; ++q)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int u = u0 + 32 * k + lane;
-          if (q < live && to[q] != nullptr && u < units) v[q][k] = from[q][u];
-        }
-#pragma unroll
-      for (int q = 0; q < kRows; ++q)
-#pragma unroll
-        for (int k = 0; k < 3; ++k) {
-          const int u = u0 + 32 * k + lane;
-          if (q < live && to[q] != nullptr && u < units) to[q][u] = v[q][k];
-        }
+    const int to = pairs[2 * lb * stride + li], from = pairs[(2 * lb + 1) * stride + li];
+    const int32_t* pages = page_table + (long long)lb * max_pages;
+    const int pt = pages[to / page_size], pf = pages[from / page_size];
+    long long row_to = (long long)pt * page_size + to % page_size;
+    const long long row_from = (long long)pf * page_size + from % page_size;
+    if (pt < 0 || pt >= n_pages || pf < 0 || pf >= n_pages) {
+      raise_flag(kFlagBounds);
+      row_to = -1;
     }
+    if (lane < count) {
+      const long long d = lb * stride;
+      new_weights[d + to] = weights[d + from];
+      if (new_pos != nullptr) new_pos[d + to] = slot_pos != nullptr ? slot_pos[d + from] : from;
+    }
+    for (int q0 = 0; q0 < count; q0 += kRows) {
+      U* dst[kRows];
+      const U* src[kRows];
 #pragma unroll
-    for (int q = 0; q < kRows; ++q)
-      if (q < live && lane == q) {
-        const long long d = bb[q] * stride;
-        new_weights[d + p[q].x] = weights[d + p[q].y];
-        if (new_pos != nullptr)
-          new_pos[d + p[q].x] = slot_pos != nullptr ? slot_pos[d + p[q].y] : p[q].y;
+      for (int q = 0; q < kRows; ++q) {
+        const long long rt = __shfl_sync(0xffffffffu, row_to, q0 + q);
+        const long long rf = __shfl_sync(0xffffffffu, row_from, q0 + q);
+        dst[q] = q0 + q < count && rt >= 0 ? pool + rt * units : nullptr;
+        src[q] = pool + rf * units;
       }
+      for (int u0 = 0; u0 < units; u0 += 96) {
+        U v[kRows][3];
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const int u = u0 + 32 * k + lane;
+            if (dst[q] != nullptr && u < units) v[q][k] = src[q][u];
+          }
+#pragma unroll
+        for (int q = 0; q < kRows; ++q)
+#pragma unroll
+          for (int k = 0; k < 3; ++k) {
+            const int u = u0 + 32 * k + lane;
+            if (dst[q] != nullptr && u < units) dst[q][u] = v[q][k];
+          }
+      }
+    }
+    // the pair after the last lane's
+    b = __shfl_sync(0xffffffffu, lb, 31);
+    i = __shfl_sync(0xffffffffu, li, 31) + 1;
+    n = __shfl_sync(0xffffffffu, ln, 31);
   }
 }
 
