@@ -27,6 +27,8 @@
 //     weights of a longer run's rest again).  Ranks
 //     within a run come from ballots; the runs' counts meet in one scan per
 //     block and one exchange per cluster.
+//   * Where at most three leave, the least (key, slot) is found that many
+//     times instead, each by a minimum over registers, warps and blocks.
 //   * Among equal keys the lowest slots leave.  Their ranks take another
 //     exchange, made only where some of the equal ones stay.
 //   * It writes the vacated and the moving slots, the weights and positions
@@ -41,7 +43,7 @@
 //
 // Bound: the plan by latency (loads, then three to six cluster barriers) and by
 // instruction issue (32 warps on one SM), the move by memory bandwidth.
-// Measured in a graph: one token of 16 x 4097 12.3 us (plan 9.5), 64 sequences
+// Measured in a graph: one token of 16 x 4097 8.0 us, 64 sequences
 // of 129 to 32769 tokens to 30 % 52 us (plan 18.5), 4 x 131072 halved 76 us
 // (plan 21).
 #pragma once
@@ -57,6 +59,11 @@ constexpr int kEvictBins = 2048;
 // Keys a thread can hold: 8 where that is enough (fewer instructions per
 // thread: with 1024 threads the plan is bound by instruction issue), else 16.
 constexpr int kEvictFewKeys = 8, kEvictKeys = 16;
+// Up to so many tokens of a sequence leave one after the other, as when every
+// decode step adds a few to a full budget: 1.3 us each for 4097 tokens (one
+// token: 8.0 us with its move against 12.3 by the histograms, two 9.8, four
+// 12.2), 2.8 us for 131072 (12.6 against 23.3, four 21.5).
+constexpr int kEvictPicks = 3;
 constexpr int kEvictGroups = 2048;                          // sequence groups of the move
 
 struct EvictArgs {
@@ -145,6 +152,13 @@ __device__ __forceinline__ int warp_inclusive(int x, int lane) {
   return x;
 }
 
+__device__ __forceinline__ unsigned long long warp_least(unsigned long long x) {
+  const uint32_t hi = (uint32_t)(x >> 32);
+  const uint32_t h = __reduce_min_sync(0xffffffffu, hi);
+  const uint32_t l = __reduce_min_sync(0xffffffffu, hi == h ? (uint32_t)x : 0xffffffffu);
+  return (unsigned long long)h << 32 | l;
+}
+
 // Exclusive prefix over the warps of the cluster's blocks, in slot order, of
 // one pair of counts per warp; *total receives the sums.  Every thread of the
 // cluster calls it, each call with a cell of its own.
@@ -186,6 +200,8 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   __shared__ int4 lists[32][32];                     // per warp: what its groups list
   __shared__ int4 pick_sh;                           // digit, keys below it, keys with it, sum
   __shared__ int max_sh;
+  __shared__ __align__(8) unsigned long long picks[kEvictPicks][32], block_pick[kEvictPicks];
+  __shared__ int picked[kEvictPicks];                // slots that leave, where few do
   const uint32_t n = cluster_nctas(), rank = cluster_ctarank();
   const int b = blockIdx.x / n;
   const int warp = __shfl_sync(0xffffffffu, threadIdx.x >> 5, 0);   // (uniform to the compiler)
@@ -275,9 +291,39 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
     for (int i = 0; i < kKeys; ++i)
       key[i] = s0 + 32 * i + lane < s1 ? key_of(__uint_as_float(key[i]), pos[i]) : kEvictKept;
 
+    if (over <= kEvictPicks) {
+      // ---- few leave: the least (key, slot), one after the other ----
+      unsigned long long least = 0;          // the next one to leave is this or above it
+      for (; n_out < over; ++n_out) {
+        unsigned long long m = ~0ull;
+        each([&](int i, uint32_t k) {
+          const unsigned long long x =
+              (unsigned long long)k << 32 | (uint32_t)(s0 + 32 * i + lane);
+          if (k != kEvictKept && x >= least && x < m) m = x;
+        });
+        m = warp_least(m);
+        if (lane == 0) picks[n_out][warp] = m;
+        __syncthreads();
+        m = warp_least(picks[n_out][lane]);
+        if (n > 1) {
+          if (threadIdx.x == 0) block_pick[n_out] = m;
+          cluster_sync();
+          unsigned long long x = ~0ull;
+          if (lane < n)
+            asm volatile("ld.shared::cluster.u64 %0, [%1];"
+                         : "=l"(x)
+                         : "r"(mapa_shared(smem_u32(&block_pick[n_out]), lane)));
+          m = warp_least(x);
+        }
+        if (m == ~0ull) break;               // (uniform: nothing is free)
+        if (threadIdx.x == 0) picked[n_out] = (int)(uint32_t)m;
+        least = m + 1;
+      }
+    }
     // ---- the n_out-th smallest key, digit by digit ----
 #pragma unroll
     for (int pass = 0; pass < 3; ++pass) {
+      if (over <= kEvictPicks) break;
       const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0;
       const uint32_t mask = pass == 2 ? 0x3FFu : 0x7FFu;
       const uint32_t known = pass == 0 ? 0u : pass == 1 ? 0xFFE00000u : 0xFFFFFC00u;
@@ -328,7 +374,25 @@ __global__ void __launch_bounds__(kEvictThreads) evict_plan_kernel(const EvictAr
   }
   const int new_len = Lc - n_out;
   const uint32_t lower = (1u << lane) - 1;
-  if (n_out > 0) {
+  if (over <= kEvictPicks) {
+    // the vacated slots in order, and the slots behind the new end that stay
+    if (rank == 0 && threadIdx.x == 0) {
+      int32_t* holes = a.pairs + 2 * b * a.stride;
+      int n_move = 0;
+      for (int at = -1;;) {
+        int hole = new_len;
+        for (int i = 0; i < n_out; ++i)
+          if (picked[i] > at) hole = min(hole, picked[i]);
+        if (hole == new_len) break;
+        holes[n_hole++] = at = hole;
+      }
+      for (int t = new_len; t < Lc; ++t) {
+        bool out = false;
+        for (int i = 0; i < n_out; ++i) out |= picked[i] == t;
+        if (!out) holes[a.stride + n_move++] = t;
+      }
+    }
+  } else if (n_out > 0) {
     // ---- ranks of the equal keys, where some of them stay ----
     int eq0 = 0;
     if (!all_leave) {

@@ -109,6 +109,30 @@ def test_small_lengths(kind, placed):
 
 
 @gpu
+@pytest.mark.parametrize("stride,kind", [(70, "spread"), (70, "ties"), (70, "equal"), (70, "odd"), (4097, "spread"),
+                                         (9000, "ties"), (40000, "odd")])
+@pytest.mark.parametrize("alias", [False, True])
+def test_a_few_leave(kind, stride, alias):
+    """The numbers around which sequences turn from one selection to the other, in one batch; with
+    fewer free slots than should leave, the slots behind the new end leaving, and none free."""
+    rng = np.random.default_rng(13)
+    lens = [stride, stride - 1, 5, 4, 1, 3, 0]
+    w = draw_w(rng, lens, kind)
+    pos = [rng.permutation(3 * L)[:L] for L in lens]
+    d = dims("bf16", dc=8, dr=0, page=16)
+    run(d, lens, [L - 1 for L in lens], w, pos, 0, 0, alias=alias)
+    run(d, lens, [L - 3 for L in lens], w, pos, 4, 3, alias=alias)
+    run(d, lens, [L - 1 - b % 5 for b, L in enumerate(lens)], w, None, 0, 1, alias=alias)
+    for b, L in enumerate(lens):                       # the lightest ones last
+        w[b][max(0, L - 3):] = -np.inf
+    for drop in (2, 3, 4):
+        run(d, lens, [L - drop for L in lens], w, None, 0, 0, alias=alias)
+    run(d, lens, [L - 3 for L in lens], w, None, 0, 2, alias=alias)
+    run(d, lens, [L - 3 for L in lens], w, None, stride - 2, 0, alias=alias)          # two free
+    run(d, lens, [L - 3 for L in lens], w, None, stride, 0, alias=alias)              # none
+
+
+@gpu
 @pytest.mark.parametrize("n_recent", [0, 1, 7, 2 ** 31 - 1])
 def test_the_last_position_there_is(n_recent):
     rng = np.random.default_rng(12)
