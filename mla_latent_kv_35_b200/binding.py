@@ -190,12 +190,12 @@ def _dev(*ts):
 
 
 def _addr(dims: MLADims) -> int:
-    """Address of the dims struct, built once per MLADims."""
+    """Address of the dims struct, built once per MLADims.  Threads whose first calls meet all take
+    the struct that is kept: one of their own would be gone before the call has read it."""
     c = dims.__dict__.get("_c")
     if c is None:
         s = dims.c()
-        c = (ctypes.addressof(s), s)
-        object.__setattr__(dims, "_c", c)
+        c = dims.__dict__.setdefault("_c", (ctypes.addressof(s), s))
     return c[0]
 
 
