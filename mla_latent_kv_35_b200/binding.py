@@ -201,7 +201,9 @@ def _addr(dims: MLADims) -> int:
 
 def _native():
     """The checks and calls of the operators around the cache (csrc/pycall.cpp), bound to lib():
-    tensors on the current device, contiguous, of the right type and large enough, or ValueError."""
+    tensors on the current device, contiguous, of the right type and large enough, or ValueError.
+    (y, q and ckr of mla_norm_rope may be views of rows at the stride they come with, contiguous
+    within a row.)"""
     if _lib is None:
         lib()
     return _pycall

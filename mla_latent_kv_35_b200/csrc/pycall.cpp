@@ -117,24 +117,31 @@ struct Args {
     return !ok || o == Py_None ? nullptr : here(what, o, type, numel);
   }
 
-  // address of `rows` rows of `width` elements, `stride` apart; the tensor is a
-  // view of them whose storage holds them all
+  // address of `rows` rows of `width` elements, `stride` apart: a contiguous
+  // tensor that holds them all, or a view whose first dimension are rows at
+  // that stride, each contiguous and wide enough
   void* rows(const char* what, PyObject* o, at::ScalarType type, long long rows, long long width,
              long long stride) {
     const at::Tensor* t = placed(what, o, type);
     if (t == nullptr) return nullptr;
-    if (!(stride >= width && t->numel() >= rows * stride && t->is_contiguous())) {
-      const long long need =
-          rows > 0 ? (t->storage_offset() + (rows - 1) * stride + width) * t->element_size() : 0;
-      if (stride < width || (long long)t->storage().nbytes() < need) {
-        PyErr_Format(PyExc_ValueError,
-                     "%s: the tensor does not hold %lld rows of %lld at stride %lld", what, rows,
-                     width, stride);
-        ok = false;
-        return nullptr;
-      }
+    if (stride < width || !(rows <= 0 || holds_rows(*t, rows, width, stride))) {
+      PyErr_Format(PyExc_ValueError,
+                   "%s: the tensor does not hold %lld rows of %lld at stride %lld", what, rows,
+                   width, stride);
+      ok = false;
+      return nullptr;
     }
     return t->data_ptr();
+  }
+  static bool holds_rows(const at::Tensor& t, long long rows, long long width, long long stride) {
+    if (t.is_contiguous()) return t.numel() >= (rows - 1) * stride + width;
+    if (t.dim() < 2 || t.size(0) < rows || (rows > 1 && t.stride(0) != stride)) return false;
+    long long inner = 1;                    // numbers of a row's last dimensions
+    for (long long i = t.dim() - 1; i > 0; --i) {
+      if (t.size(i) != 1 && t.stride(i) != inner) return false;
+      inner *= t.size(i);
+    }
+    return inner >= width;
   }
 
   // the C call's status; other Python threads run meanwhile

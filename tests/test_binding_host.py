@@ -4,6 +4,9 @@ import ctypes
 import sys
 import threading
 
+import pytest
+import torch
+
 from mla_latent_kv_35_b200 import binding as B
 
 
@@ -50,3 +53,59 @@ def test_first_calls_of_four_threads():
             assert len(seen) == 4 and set(seen) == {B._addr(d)}
     finally:
         sys.setswitchinterval(old)
+
+
+H, DN, DC, DR, PAGE = 4, 16, 32, 8, 64
+DQK, D = DN + DR, DC + DR
+Y = H * DQK + D
+
+
+@pytest.fixture
+def norm(monkeypatch):
+    """norm(T=, y=, ...) calls mla_norm_rope on CPU tensors.  It reaches the library only with an eps that
+    the library refuses, so nothing is launched."""
+    from mla_latent_kv_35_b200 import build
+    build.build()
+    monkeypatch.setattr(B, "_where", lambda: (-1, 0))
+
+    def call(T=3, **kw):
+        z = lambda *s: torch.zeros(s, dtype=torch.bfloat16)  # noqa: E731
+        a = dict(y=z(T, Y), ys=Y, q=z(T, H * DQK), qs=H * DQK, ckr=None, cs=0)
+        a.update(kw)
+        B.mla_norm_rope(dims(), a["y"], a["ys"], None, None, None, -1.0, torch.zeros(T, dtype=torch.int32), None,
+                        None, None, 0, None, 0, a["q"], a["qs"], None, a["ckr"], a["cs"], T)
+    return call
+
+
+def rows(n, width, wide=0):
+    return torch.zeros((n, width + wide), dtype=torch.bfloat16)[:, :width]
+
+
+@pytest.mark.parametrize("name,stride,width", [("y", "ys", Y), ("q", "qs", H * DQK), ("ckr", "cs", D)])
+def test_rows_at_a_stride_lie_within_their_tensor(norm, name, stride, width):
+    def refused(t, s, T=3):
+        with pytest.raises(ValueError, match=f"{name}: the tensor does not hold {T} rows"):
+            norm(T, **{name: t, stride: s})
+
+    def reaches_the_library(t, s, T=3):
+        with pytest.raises(B.MLAError):
+            norm(T, **{name: t, stride: s})
+    big = rows(8, width + 5)
+    reaches_the_library(rows(3, width), width)
+    reaches_the_library(rows(3, width, 9), width + 9)                    # a view of wider rows
+    reaches_the_library(big[:, 5:], width + 5, 8)                        # which end with the storage
+    reaches_the_library(big[2:5, 5:], width + 5)
+    reaches_the_library(big.view(-1)[:2 * (width + 5) + width], width + 5)   # flat, the last row short
+    reaches_the_library(rows(3, width).view(3, -1, 1, width // 2), width)
+    reaches_the_library(big[1:2, 5:], width, 1)                          # one row: any stride
+    reaches_the_library(big[1:3, 5:], width, 1)
+    refused(big[:2], width + 5)                                          # fewer rows than tokens
+    refused(big[:2, 5:], width + 5)
+    refused(big.view(-1)[:2 * (width + 5) + width - 1], width + 5)
+    refused(big[:, 6:], width + 5)                                       # rows too short
+    refused(big[:, 5:], width)                                           # not the view's stride
+    refused(big[::2, 5:], width + 5)
+    refused(rows(width, 3).t(), width)                                   # columns as rows
+    refused(rows(3, 2 * width)[:, ::2], 2 * width)                       # every other number
+    refused(rows(1, width).expand(3, width), width)                      # one row for all
+    reaches_the_library(big[:0], width, 0)
