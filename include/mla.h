@@ -493,7 +493,8 @@ mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, 
  * new_lens[b] on keep their contents; whole pages among them may be reused.
  * pool: device [n_pages, page_size] rows of dims' type, or of
  * MLA_FP8_ROW_BYTES bytes where fp8_rows is not 0 (8-bit cache; else
- * MLA_ERR_UNSUPPORTED).  Rows move in place: no page may belong to two
+ * MLA_ERR_UNSUPPORTED), at an even address (on a 16-byte boundary rows move
+ * fastest).  Rows move in place: no page may belong to two
  * sequences.  weights, new_weights: device fp32 [B, stride]; slot_pos,
  * new_pos: device int32 [B, stride], each may be NULL (new_pos NULL: positions
  * are not kept); entries < new_lens[b] of new_weights and new_pos are written.

@@ -1033,7 +1033,9 @@ mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp
   if (!pool || !page_table || !seq_lens || !weights || !budget || !new_weights || !new_lens ||
       !workspace)
     return MLA_ERR_INVALID_ARG;
+  // rows move in units of 16 bytes, or of two
   if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0 ||
+      (reinterpret_cast<uintptr_t>(pool) & 1u) != 0 ||
       ws_bytes < mla_cache_evict_workspace_size(dims, B, stride))
     return MLA_ERR_INVALID_ARG;
   cudaStream_t st = as_stream(stream);

@@ -109,3 +109,15 @@ def test_rows_at_a_stride_lie_within_their_tensor(norm, name, stride, width):
     refused(rows(3, 2 * width)[:, ::2], 2 * width)                       # every other number
     refused(rows(1, width).expand(3, width), width)                      # one row for all
     reaches_the_library(big[:0], width, 0)
+
+
+@pytest.mark.parametrize("fp8", [0, 1])
+def test_eviction_refuses_a_pool_at_an_odd_address(fp8):
+    """A slice of a uint8 tensor may begin at any byte; rows move in units of two bytes at least."""
+    from mla_latent_kv_35_b200 import build
+    build.build()
+    d = B.MLADims(4, 128, 512, 64, 128, 64, 64, 0.1, 10000.0, "bf16")
+    x = 1 << 12
+    for pool in (x + 1, x + 15):
+        assert B.lib().mla_cache_evict(ctypes.byref(d.c()), pool, 4, fp8, x, 2, x, 2, x, 0, 100, x, 0, 0, x, 0, x,
+                                       x, 1 << 20, 0) == 1
