@@ -751,7 +751,8 @@ mla_status mla_out_proj(const mla_dims* dims, const float* o_lat, const void* w_
   auto up = [](size_t x) { return (x + 255) & ~(size_t)255; };
   __nv_bfloat16* olb = static_cast<__nv_bfloat16*>(scratch);
   const long long n = (long long)T * H * dc;
-  cast_f32_bf16_kernel<<<(unsigned)((n / 4 + 255) / 256 + 1), 256, 0, st>>>(o_lat, olb, n);
+  cast_f32_bf16_kernel<<<(unsigned)((n / 4 + 255) / 256 + 1), 256, 0, st>>>(o_lat, olb, n,
+                                                                           aligned16(o_lat));
   MLA_TRY(check_launch());
   return out_proj_bf16(dims, olb, w_uv, w_o,
                        static_cast<char*>(scratch) + up((size_t)T * H * dc * 2), out, T, st);
@@ -795,8 +796,9 @@ static mla_status out_proj_bf16(const mla_dims* dims, const __nv_bfloat16* olb, 
   MLA_TRY(launch_tc_gemm(w_o, false, 0, o, (long long)H * dv, 0, dm, T, H * dv, 1, parts, 0, dm, 1,
                          kOutF32Split, st, nullptr, &splits));
   const long long n_out = (long long)T * dm;
+  const bool wide = n_out % 4 == 0 && aligned16(out);
   sum_splits_kernel<<<(unsigned)((n_out / 4 + 255) / 256 + 1), 256, 0, st>>>(parts, splits, n_out,
-                                                                             out);
+                                                                             out, wide);
   return check_launch();
 }
 

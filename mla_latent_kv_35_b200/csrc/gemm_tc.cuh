@@ -264,9 +264,11 @@ __global__ void __launch_bounds__(128, 1) gemm_tc_kernel(const __grid_constant__
 }
 
 // out[i] = sum over s = 0 .. splits-1 of parts[s * n + i], in that order.
-__global__ void sum_splits_kernel(const float* parts, int splits, long long n, float* out) {
+// wide: every slice of parts and out start on a 16-byte boundary.
+__global__ void sum_splits_kernel(const float* parts, int splits, long long n, float* out,
+                                  bool wide) {
   const long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (i + 3 < n) {
+  if (wide && i + 3 < n) {
     float4 acc = *reinterpret_cast<const float4*>(parts + i);
     for (int s = 1; s < splits; ++s) {
       const float4 v = *reinterpret_cast<const float4*>(parts + s * n + i);
@@ -274,7 +276,7 @@ __global__ void sum_splits_kernel(const float* parts, int splits, long long n, f
     }
     *reinterpret_cast<float4*>(out + i) = acc;
   } else {
-    for (long long k = i; k < n; ++k) {
+    for (long long k = i; k < min(n, i + 4); ++k) {
       float acc = parts[k];
       for (int s = 1; s < splits; ++s) acc += parts[s * n + k];
       out[k] = acc;

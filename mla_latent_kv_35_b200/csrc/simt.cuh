@@ -126,16 +126,17 @@ __global__ void append_kernel(const E* c, long long cs_tok, const E* kr, long lo
     row[e] = e < d_c ? c[t * cs_tok + e] : kr[t * ks_tok + (e - d_c)];
 }
 
-__global__ void cast_f32_bf16_kernel(const float* x, __nv_bfloat16* y, long long n) {
+// wide: x starts on a 16-byte boundary (y always does).
+__global__ void cast_f32_bf16_kernel(const float* x, __nv_bfloat16* y, long long n, bool wide) {
   long long i = ((long long)blockIdx.x * blockDim.x + threadIdx.x) * 4;
-  if (i + 3 < n) {
+  if (wide && i + 3 < n) {
     float4 v = *reinterpret_cast<const float4*>(x + i);
     uint2 o;
     o.x = pack_bf16x2(v.x, v.y);
     o.y = pack_bf16x2(v.z, v.w);
     *reinterpret_cast<uint2*>(y + i) = o;
   } else {
-    for (; i < n; ++i) y[i] = __float2bfloat16_rn(x[i]);
+    for (const long long end = min(n, i + 4); i < end; ++i) y[i] = __float2bfloat16_rn(x[i]);
   }
 }
 

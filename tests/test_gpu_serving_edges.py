@@ -1,0 +1,60 @@
+"""Calls at the edges of what the operators around the cache allow: NaN among the inputs, offsets and
+pages that break their rules, evictions one after the other, appends behind an eviction, outputs at odd
+addresses."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle
+from mla_latent_kv_35_b200 import binding as B
+from mla_latent_kv_35_b200.engine import DecodePipeline, PrefillPipeline
+from gpu_util import check, dims, ensure_lib, q, status, to_dev, to_np
+from serving_util import DEV, bits, i32, paged
+import test_gpu_attn_weights as tw
+import test_gpu_chunk as tc
+from test_gpu_serving import Reference, make, tokens
+
+gpu = pytest.mark.gpu
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    if torch.cuda.is_available():
+        ensure_lib()
+        B.mla_get_device_status()
+
+
+@gpu
+@pytest.mark.parametrize("dm,shift,T", [(256, 1, 5), (256, 2, 130), (130, 0, 3), (131, 0, 1), (133, 3, 64),
+                                        (5120, 1, 2)])
+def test_out_proj_at_any_address_and_width(dm, shift, T):
+    """Outputs at any float's address and a model width that is no multiple of four, with and without
+    a split of the product, are those of the aligned call."""
+    d = dims("bf16", H=16, dm=dm)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(dm + T)
+    mk = lambda *n: torch.randn(n, generator=g, device=DEV).bfloat16()  # noqa: E731
+    o, w_uv, w_o = mk(T, 16, 512), mk(16, 128, 512), mk(dm, 16 * 128)
+    wide = dims("bf16", H=16, dm=-(-dm // 8) * 8)
+    w_wide = torch.zeros((wide.d_model, 16 * 128), dtype=torch.bfloat16, device=DEV)
+    w_wide[:dm] = w_o
+    ref = torch.empty((T, wide.d_model), device=DEV)
+    s = torch.empty(B.mla_out_proj_bf16_scratch_size(wide, T), dtype=torch.uint8, device=DEV)
+    B.mla_out_proj_bf16(wide, o, w_uv, w_wide, s, ref, T)
+    store = torch.full((T * dm + shift + 1,), 7.0, device=DEV)
+    out = store[shift:shift + T * dm].view(T, dm)
+    s = torch.empty(B.mla_out_proj_bf16_scratch_size(d, T), dtype=torch.uint8, device=DEV)
+    B.mla_out_proj_bf16(d, o, w_uv, w_o, s, out, T)
+    assert status() == 0
+    assert torch.equal(out, ref[:, :dm])
+    assert (store[:shift] == 7).all() and store[-1] == 7
+    # and of fp32 rows, at an odd address too
+    of = torch.full((T * 16 * 512 + shift,), 0.0, device=DEV)[shift:].view(T, 16, 512)
+    of.copy_(o)
+    out.fill_(0)
+    s = torch.empty(B.mla_out_proj_scratch_size(d, T), dtype=torch.uint8, device=DEV)
+    B.mla_out_proj(d, of, w_uv, w_o, s, out, T)
+    assert status() == 0
+    assert torch.equal(out, ref[:, :dm]) and (store[:shift] == 7).all() and store[-1] == 7
