@@ -178,7 +178,7 @@ size_t mla_decode_fp8_workspace_size(const mla_dims* dims, int B, int S_q,
  * product, and the value product takes 64 * p * s rounded to half as its
  * weights (the 64 keeps them in half's normal range; it is divided out);
  * accumulation is fp32.  Needs dtype MLA_BF16, d_latent == 512, d_rope == 64, page_size ==
- * 64 (else MLA_ERR_UNSUPPORTED), 1 <= S_q <= 2, a 256-byte aligned workspace
+ * 64, scale >= 0 (else MLA_ERR_UNSUPPORTED), 1 <= S_q <= 2, a 256-byte aligned workspace
  * of mla_decode_fp8_workspace_size bytes, and 16-byte aligned qbuf and
  * pool8.  Device-side errors as for mla_decode. */
 mla_status mla_decode_fp8(const mla_dims* dims, const void* qbuf, const void* pool8,
@@ -251,7 +251,8 @@ size_t mla_decode_workspace_size(const mla_dims* dims, int B, int S_q,
  * [B, S_q, H, d_latent]; lse: device fp32 [B, S_q, H]; workspace: device,
  * >= mla_decode_workspace_size bytes, 256-byte aligned, contents ignored.
  * bf16 requires d_latent == 512, d_rope == 64, page_size == 64, and
- * S_q*H % 128 == 0; 1 <= S_q <= 2 in both modes. */
+ * S_q*H % 128 == 0; 1 <= S_q <= 2 in both modes.  A negative scale takes the
+ * CUDA-core kernel, whatever the type. */
 mla_status mla_decode(const mla_dims* dims, const void* qbuf, const void* pool,
                       int n_pages, const int32_t* page_table, int max_pages,
                       const int32_t* seq_lens, int B, int S_q, int num_workers,
@@ -374,7 +375,8 @@ mla_status mla_prefill_rebuild_kv(const mla_dims* dims, const void* pool, int n_
  * o: device bf16 [T, H, d_v] (out, the input of the W_O projection, which
  * mla_project applies); lse: device fp32 [T, H] (out).  0 <= T <= L
  * (T = 0 is a no-op); q_stride_tok % 8 == 0; shapes as for
- * mla_prefill_rebuild_kv; all buffers 16-byte aligned. */
+ * mla_prefill_rebuild_kv; all buffers 16-byte aligned; scale >= 0 (else
+ * MLA_ERR_UNSUPPORTED). */
 mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stride_tok,
                                  const void* ctx, const void* k_nope, const void* v, int T,
                                  int L, void* o, float* lse, void* stream);
@@ -396,8 +398,8 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
  * value product and o_lat when it is stored.  workspace: device, >=
  * mla_chunk_attention_workspace_size bytes, 256-byte aligned, contents
  * ignored.  qbuf, pool and o_lat 16-byte aligned.  Needs dtype MLA_BF16,
- * d_latent == 512, d_rope == 64, page_size == 64 (else MLA_ERR_UNSUPPORTED,
- * workspace size 0), any n_heads, total_q * H + 128 * B < 2^31, and
+ * d_latent == 512, d_rope == 64, page_size == 64, scale >= 0 (else
+ * MLA_ERR_UNSUPPORTED, workspace size 0), any n_heads, total_q * H + 128 * B < 2^31, and
  * (total_q * H / 128 + B) * (max_pages / 4, rounded up) < 2^31.  A cu_q that
  * breaks its rules anywhere leaves every row as it was; a chunk with L < T_b
  * or L > max_pages*page_size gets o_lat = 0, lse = -inf; both raise

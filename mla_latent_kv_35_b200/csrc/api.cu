@@ -50,6 +50,11 @@ bool dims_ok(const mla_dims* d) {
          (d->dtype == MLA_F32 || d->dtype == MLA_BF16) && std::isfinite(d->scale);
 }
 
+// The tensor-core softmaxes scale the greatest product of a row and block; with
+// a negative scale that is the least score, and of a row that sees nothing of
+// the block (-inf) it is +inf.
+bool scale_negative(const mla_dims* d) { return d->scale < 0.f; }
+
 int sm_count() {
   int dev = 0, n = 0;
   cudaGetDevice(&dev);
@@ -306,11 +311,12 @@ constexpr int kBlockTokensSimt = 128;
 // The tensor-core kernel covers every bf16 shape with DeepSeek-V2's cache
 // row (512 + 64) and 64-token pages; query blocks of fewer than 128 rows
 // (S_q * H < 128, or the last block of a sequence) are padded to the MMA's
-// 128 rows, whose extra rows are computed and dropped.
+// 128 rows, whose extra rows are computed and dropped.  It takes a block's
+// greatest score before the scale, so a negative scale goes to the CUDA cores.
 bool use_tc_decode(const mla_dims* d, int S_q) {
   (void)S_q;
   return kDecodeTcReady && d->dtype == MLA_BF16 && d->d_latent == 512 && d->d_rope == 64 &&
-         d->page_size == 64;
+         d->page_size == 64 && !scale_negative(d);
 }
 
 struct DecodeLayout {
@@ -639,7 +645,9 @@ static size_t fp8_q16_offset(const mla_dims* dims, int B, int S_q, int num_worke
 }
 
 size_t mla_decode_fp8_workspace_size(const mla_dims* dims, int B, int S_q, int num_workers) {
-  if (!dims_ok(dims) || B < 0 || S_q < 1 || num_workers < 0 || !fp8_dims_ok(dims)) return 0;
+  if (!dims_ok(dims) || B < 0 || S_q < 1 || num_workers < 0 || !fp8_dims_ok(dims) ||
+      scale_negative(dims))
+    return 0;
   return fp8_q16_offset(dims, B, S_q, num_workers) +
          (((size_t)B * S_q * dims->n_heads * 576 * 2 + 255) & ~(size_t)255);
 }
@@ -652,7 +660,8 @@ mla_status mla_decode_fp8(const mla_dims* dims, const void* qbuf, const void* po
   if (!dims_ok(dims) || B < 0 || S_q < 1 || S_q > 2 || num_workers < 0 || n_pages < 1 ||
       max_pages < 1)
     return MLA_ERR_INVALID_ARG;
-  if (!fp8_dims_ok(dims) || dims->page_size != 64) return MLA_ERR_UNSUPPORTED;
+  if (!fp8_dims_ok(dims) || dims->page_size != 64 || scale_negative(dims))
+    return MLA_ERR_UNSUPPORTED;
   if (B == 0) return MLA_OK;
   if (!qbuf || !pool8 || !page_table || !seq_lens || !workspace || !o_lat || !lse)
     return MLA_ERR_INVALID_ARG;
@@ -841,7 +850,7 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
                                  const void* ctx, const void* k_nope, const void* v, int T,
                                  int L, void* o, float* lse, void* stream) {
   if (!dims_ok(dims) || T < 0 || L < T) return MLA_ERR_INVALID_ARG;
-  if (!prefill_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
+  if (!prefill_dims_ok(dims) || scale_negative(dims)) return MLA_ERR_UNSUPPORTED;
   if (T == 0) return MLA_OK;
   const int H = dims->n_heads;
   if (!q || !ctx || !k_nope || !v || !o || !lse) return MLA_ERR_INVALID_ARG;
@@ -881,7 +890,9 @@ static bool chunk_pages_ok(const mla_dims* d, int B, int total_q, int max_pages)
 }
 
 size_t mla_chunk_attention_workspace_size(const mla_dims* dims, int B, int total_q, int max_q) {
-  if (!dims_ok(dims) || !chunk_dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q)) return 0;
+  if (!dims_ok(dims) || !chunk_dims_ok(dims) || scale_negative(dims) ||
+      !chunk_sizes_ok(dims, B, total_q, max_q))
+    return 0;
   return chunk_layout(total_q, B, dims->n_heads, sm_count() / 2).total;
 }
 
@@ -893,7 +904,7 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
   if (!dims_ok(dims) || !chunk_sizes_ok(dims, B, total_q, max_q) || n_pages < 1 ||
       !chunk_pages_ok(dims, B, total_q, max_pages))
     return MLA_ERR_INVALID_ARG;
-  if (!chunk_dims_ok(dims)) return MLA_ERR_UNSUPPORTED;
+  if (!chunk_dims_ok(dims) || scale_negative(dims)) return MLA_ERR_UNSUPPORTED;
   if (B == 0 || total_q == 0) return MLA_OK;
   if (!qbuf || !cu_q || !pool || !page_table || !seq_lens || !workspace || !o_lat || !lse)
     return MLA_ERR_INVALID_ARG;

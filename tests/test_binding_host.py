@@ -121,3 +121,25 @@ def test_eviction_refuses_a_pool_at_an_odd_address(fp8):
     for pool in (x + 1, x + 15):
         assert B.lib().mla_cache_evict(ctypes.byref(d.c()), pool, 4, fp8, x, 2, x, 2, x, 0, 100, x, 0, 0, x, 0, x,
                                        x, 1 << 20, 0) == 1
+
+
+def test_tensor_core_softmaxes_refuse_a_negative_scale():
+    """They scale a block's greatest product, which is its least score then; the decode has another
+    kernel for it, and the gathered weights take no maximum."""
+    from mla_latent_kv_35_b200 import build
+    build.build()
+    lib, x = B.lib(), 1 << 12
+    for scale, refused in ((-0.1, True), (0.0, False), (0.1, False)):
+        d = B.MLADims(16, 128, 512, 64, 128, 64, 64, scale, 10000.0, "bf16")
+        c = ctypes.byref(d.c())
+        # zero sequences, or a workspace that is too small: nothing is launched
+        want = 2 if refused else 0
+        assert lib.mla_chunk_attention(c, 0, 0, 0, 0, 0, 4, 0, 2, 0, 0, 0, 0, 0, 0, 0) == want
+        assert lib.mla_decode_fp8(c, 0, 0, 4, 0, 2, 0, 0, 1, 0, 0, 0, 0, 0, 0) == want
+        assert lib.mla_prefill_attention(c, 0, 16 * 192, 0, 0, 0, 0, 8, 0, 0, 0) == want
+        assert lib.mla_attn_weights(c, 0, 0, 0, 0, 0, 0, 4, 0, 2, 0, 0, 0, 1.0, 0, 128, 0) == 0
+        assert (B.mla_chunk_attention_workspace_size(d, 2, 8, 4) == 0) == refused
+        assert (B.mla_decode_fp8_workspace_size(d, 2, 1) == 0) == refused
+        assert B.mla_decode_config(d, 1)[0] == (B.DECODE_KERNEL_SIMT if refused else B.DECODE_KERNEL_TC)
+    assert lib.mla_chunk_attention(ctypes.byref(B.MLADims(16, 128, 512, 64, 128, 64, 64, -0.1, 1e4, "bf16").c()),
+                                   x, x, 8, 4, x, 4, x, 2, x, 2, x, 1 << 40, x, x, 0) == 2

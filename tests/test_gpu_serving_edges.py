@@ -58,3 +58,34 @@ def test_out_proj_at_any_address_and_width(dm, shift, T):
     B.mla_out_proj(d, of, w_uv, w_o, s, out, T)
     assert status() == 0
     assert torch.equal(out, ref[:, :dm]) and (store[:shift] == 7).all() and store[-1] == 7
+
+
+@gpu
+@pytest.mark.parametrize("S_q,lens", [(1, [1, 300]), (2, [257, 513, 40])])
+def test_decode_with_a_negative_scale(S_q, lens):
+    """The decode takes scales below zero too; a row that sees nothing of a 256-token block keeps its
+    sums.  Tolerance as in test_gpu_chunk, for fp32 arithmetic: a score of 18 products in a row and 5
+    sums is off by d = 24 * 2^-24 * |scale| * sum |q k|, its exponential by 2^-17 more, and every token
+    rounds o twice."""
+    d = B.MLADims(16, 128, 512, 64, 128, 5120, 64, -0.3, 10000.0, "bf16")
+    nB = len(lens)
+    pool, table, n_pages, rows = paged(np.random.default_rng(4), lens, 576, torch.bfloat16)
+    g = torch.Generator(device=DEV)
+    g.manual_seed(S_q)
+    qb = (0.5 * torch.randn((nB, S_q, 16, 576), generator=g, device=DEV)).bfloat16()
+    o, lse = torch.empty((nB, S_q, 16, 512), device=DEV), torch.empty((nB, S_q, 16), device=DEV)
+    ws = torch.empty(B.mla_decode_workspace_size(d, nB, S_q), dtype=torch.uint8, device=DEV)
+    B.mla_decode(d, qb, pool, n_pages, table, table.shape[1], i32(lens), nB, S_q, 0, ws, o, lse)
+    assert status() == 0
+    for b, L in enumerate(lens):
+        for j in range(S_q):
+            k = torch.from_numpy(rows[b][:L - S_q + j + 1]).to(DEV)
+            x = qb[b, j].double()
+            s = x @ k.T * d.scale
+            p = torch.softmax(s, 1)
+            ref, A = p @ k[:, :512], p @ k[:, :512].abs()
+            e = 24 * 2.0 ** -24 * abs(d.scale) * (x.abs() @ k.abs().T).amax(1)
+            tol = (2 * (e + 2.0 ** -17)[:, None] + L * 2.0 ** -23) * A
+            assert ((o[b, j].double() - ref).abs() <= tol).all()
+            assert ((lse[b, j].double() - torch.logsumexp(s, 1)).abs() <=
+                    e + 2.0 ** -16 + 2.0 ** -22 * torch.logsumexp(s, 1).abs() + L * 2.0 ** -23).all()
