@@ -425,14 +425,14 @@ mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int
  * = 1 gathers, less than 1 forgets.  w_in: device fp32 [B, stride], not read
  * where it is NULL or keep is 0; w_out: device fp32 [B, stride], may be w_in;
  * entries from L on are left as they were.  A row with lse = -inf gives
- * nothing.  Products of bf16 accumulate in fp32, the sums are fp32 in a fixed
- * order (the same bits every time).  Shapes, checks and cu_q as for
- * mla_chunk_attention, but for its last bound, in place of which max_pages *
- * page_size < 2^31 - 256; stride >= every length, keep finite.  A cu_q that
- * breaks its rules leaves w_out as it was; so does, for its sequence, a
- * length < T_b or > min(stride, max_pages*page_size); both raise
- * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as
- * rows of zeros. */
+ * nothing, one with lse = NaN gives NaN to the tokens it sees.  Products of
+ * bf16 accumulate in fp32, the sums are fp32 in a fixed order (the same bits
+ * every time).  Shapes, checks and cu_q as for mla_chunk_attention, but for
+ * its last bound, in place of which max_pages * page_size < 2^31 - 256, and
+ * any scale; stride >= every length, keep finite.  A cu_q that breaks its
+ * rules leaves w_out as it was; so does, for its sequence, a length < T_b or
+ * > min(stride, max_pages*page_size); both raise MLA_ERR_BOUNDS, as does a
+ * page id outside the pool, whose tokens count as rows of zeros. */
 mla_status mla_attn_weights(const mla_dims* dims, const void* qbuf, const float* lse,
                             const int32_t* cu_q, int total_q, int max_q, const void* pool,
                             int n_pages, const int32_t* page_table, int max_pages,

@@ -41,7 +41,8 @@
 // traffic each, and two tiles for most pairs against 1.73 on average.
 //
 // Row sums: four chains per thread over 32 columns at a time, fp32.  Rows
-// whose lse is not finite give nothing (a query that saw nothing has -inf).
+// whose lse is -inf (a query that saw nothing) or +inf give nothing; one whose
+// lse is NaN gives NaN to the tokens it sees.
 // Tokens past a sequence's end compute on whatever the page holds there and
 // are not stored.
 //
@@ -497,7 +498,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
           v[i] = INFINITY;
           if (et + i * kEpiThreads < kN && r < w.T * P.H) {
             const float x = P.lse[(long long)w.q0 * P.H + r];
-            if (x > -INFINITY) v[i] = x * 1.4426950408889634f;
+            if (x != -INFINITY) v[i] = x * 1.4426950408889634f;
           }
         }
       };
@@ -557,7 +558,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
             for (int c = 0; c < 32; ++c) {
               const float l = l2[32 * g + c];
               const float p = ex2_approx(fmaf(__uint_as_float(r[c]), P.scale_log2, -l));
-              s4[c & 3] += t < lim[32 * g + c] && l < INFINITY ? p : 0.f;
+              s4[c & 3] += t < lim[32 * g + c] && l != INFINITY ? p : 0.f;
             }
           }
         }

@@ -89,3 +89,29 @@ def test_decode_with_a_negative_scale(S_q, lens):
             assert ((o[b, j].double() - ref).abs() <= tol).all()
             assert ((lse[b, j].double() - torch.logsumexp(s, 1)).abs() <=
                     e + 2.0 ** -16 + 2.0 ** -22 * torch.logsumexp(s, 1).abs() + L * 2.0 ** -23).all()
+
+
+@gpu
+@pytest.mark.parametrize("H,qs,lens", [(16, [3, 2], [200, 90]), (128, [2, 1], [300, 513]),
+                                       (128, [5, 3], [300, 70])])
+def test_a_nan_lse_reaches_every_token_its_query_sees(H, qs, lens):
+    """One (query, head) with lse = NaN, in each form of the kernel: the tokens it sees weigh NaN, the
+    later ones and the other sequence's as if that row gave nothing."""
+    d = dims("bf16", H=H)
+    pool, table, n_pages, rows = paged(np.random.default_rng(1), lens, 576, torch.bfloat16)
+    total, cu = sum(qs), i32(np.concatenate([[0], np.cumsum(qs)]))
+    qb = torch.randn((total, H, 576), device=DEV).bfloat16()
+    lse = torch.full((total, H), 8.0, device=DEV)
+    got = []
+    for bad in (-float("inf"), NAN):
+        lse[1, H - 1] = bad                            # the second query of the first sequence
+        w = torch.full((2, max(lens)), 9.0, device=DEV)
+        tw.call(d, qb, lse, cu, total, max(qs), pool, n_pages, table, i32(lens), None, 1.0, w)
+        assert status() == 0
+        got.append(w)
+    see = lens[0] - qs[0] + 2
+    assert got[1][0, :see].isnan().all()
+    assert torch.equal(got[1][0, see:], got[0][0, see:]) and torch.equal(got[1][1], got[0][1])
+    ref, tol = tw.reference(qb[:qs[0]], torch.where(lse[:qs[0]].isnan(), -float("inf"), lse[:qs[0]]), rows[0],
+                            qs[0], d.scale)
+    assert ((got[0][0, :lens[0]].double() - ref).abs() <= tol + 2.0 ** -23 * ref).all()
