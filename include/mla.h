@@ -404,8 +404,9 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
  * breaks its rules anywhere leaves every row as it was; a chunk with L < T_b
  * or L > max_pages*page_size gets o_lat = 0, lse = -inf; both raise
  * MLA_ERR_BOUNDS, as does a page id outside the pool, whose tokens count as
- * rows of zeros.  Many queries of one sequence are cheaper in the non-absorbed
- * form (mla_prefill_attention), from a few hundred on. */
+ * rows of zeros.  A query and head with NaN among its scores get o_lat and
+ * lse = NaN.  Many queries of one sequence are cheaper in the non-absorbed form
+ * (mla_prefill_attention), from a few hundred on. */
 size_t mla_chunk_attention_workspace_size(const mla_dims* dims, int B, int total_q, int max_q);
 mla_status mla_chunk_attention(const mla_dims* dims, const void* qbuf, const int32_t* cu_q,
                                int total_q, int max_q, const void* pool, int n_pages,

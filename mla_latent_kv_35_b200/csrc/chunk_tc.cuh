@@ -273,17 +273,20 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse,
   for (int i = lane; i < n; i += 32) mx = fmaxf(mx, ws_lse[slot(i)]);
 #pragma unroll
   for (int d = 16; d > 0; d >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, d));
+  // z: 0 where no piece saw anything, NaN where one had a NaN (which the
+  // maximum passes over)
+  const float m0 = mx == -INFINITY ? 0.f : mx;
   float z = 0.f;
   float4 acc[4];
 #pragma unroll
   for (int q = 0; q < 4; ++q) acc[q] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (mx != -INFINITY && live) {
-    for (int i = lane; i < n; i += 32) z += __expf(ws_lse[slot(i)] - mx);
+  for (int i = lane; i < n; i += 32) z += __expf(ws_lse[slot(i)] - m0);
 #pragma unroll
-    for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  for (int d = 16; d > 0; d >>= 1) z += __shfl_xor_sync(0xffffffffu, z, d);
+  if (z != 0.f && live) {
 #pragma unroll 2
     for (int i = u; i < n; i += wpr) {
-      const float e = __expf(ws_lse[slot(i)] - mx);
+      const float e = __expf(ws_lse[slot(i)] - m0);
       const float4* src = reinterpret_cast<const float4*>(ws_o + slot(i) * dtc::kDC);
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
@@ -309,14 +312,14 @@ __global__ void __launch_bounds__(256) chunk_combine_kernel(const float* ws_lse,
       }
   }
   if (!live) return;
-  const float inv = z > 0.f ? 1.f / z : 0.f;
+  const float inv = z != 0.f ? 1.f / z : 0.f;
   const long long row = (long long)s.q0 * H + s.row0 + r;
   uint2* dst = reinterpret_cast<uint2*>(o + row * dtc::kDC);
 #pragma unroll
   for (int q = 0; q < 4; ++q)
     dst[32 * q + lane] = make_uint2(pack_bf16x2(acc[q].x * inv, acc[q].y * inv),
                                     pack_bf16x2(acc[q].z * inv, acc[q].w * inv));
-  if (lane == 0) lse[row] = z > 0.f ? mx + logf(z) : -INFINITY;
+  if (lane == 0) lse[row] = z != 0.f ? m0 + logf(z) : -INFINITY;
 }
 
 struct ChunkLayout {

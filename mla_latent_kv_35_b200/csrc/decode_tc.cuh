@@ -833,7 +833,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
       if (named_bar_or(1, kSoftmaxThreads, !got || *abort_p)) { dead = true; break; }
       tc_fence_after();
       const float lt = red_sum[h] + red_sum[64 + h] + red_sum[128 + h] + red_sum[192 + h];
-      const float inv = lt > 0.f ? 1.f / lt : 0.f;
+      // (a ragged row with NaN among its scores: NaN, in every piece of it)
+      const float inv = (kRagged ? lt != 0.f : lt > 0.f) ? 1.f / lt : 0.f;
+      const float lse = (kRagged ? lt != 0.f : lt > 0.f)
+                            ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
       // this warp writes latent half n = ch of its lanes: columns
       // 256n + 128hh + [0, 128)
       if constexpr (kRagged) {
@@ -862,8 +865,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
             }
             store_rows32(sx_warp, w, dst + 128 * cc, kDC * 2, valid, lane);
           }
-          if (live && pb == 0)
-            P.lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+          if (live && pb == 0) P.lse[row] = lse;
           __syncwarp();
           named_bar_sync(1, kSoftmaxThreads);  // red_sum is rewritten by the next piece
           tc_fence_before();
@@ -886,8 +888,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(dtc::kThreads, 1)
         for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * inv);
         store_rows32(sx_warp, r, dst + 128 * cc, kDC * 4, 32, lane);
       }
-      if (pb == 0)
-        P.ws_lse[row] = lt > 0.f ? (m + log2f(lt)) * 0.69314718055994531f : -INFINITY;
+      if (pb == 0) P.ws_lse[row] = lse;
       named_bar_sync(1, kSoftmaxThreads);  // red_sum is rewritten by the next piece
       tc_fence_before();
       __syncwarp();

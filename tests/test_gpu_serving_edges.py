@@ -115,3 +115,25 @@ def test_a_nan_lse_reaches_every_token_its_query_sees(H, qs, lens):
     ref, tol = tw.reference(qb[:qs[0]], torch.where(lse[:qs[0]].isnan(), -float("inf"), lse[:qs[0]]), rows[0],
                             qs[0], d.scale)
     assert ((got[0][0, :lens[0]].double() - ref).abs() <= tol + 2.0 ** -23 * ref).all()
+
+
+@gpu
+@pytest.mark.parametrize("H,qs,lens", [(16, [3, 1], [200, 90]), (16, [1, 2], [30000, 70]),
+                                       (128, [2, 3], [9000, 300]), (128, [40, 1], [5000, 20000])])
+def test_a_nan_query_gives_nan_however_it_is_split(H, qs, lens):
+    """Row blocks that one worker serves and ones that many share: o and lse of a query with a NaN are
+    NaN, every other row keeps its bits."""
+    d = dims("bf16", H=H)
+    pool, table, n_pages, _ = paged(np.random.default_rng(2), lens, 576, torch.bfloat16)
+    total, cu = sum(qs), i32(np.concatenate([[0], np.cumsum(qs)]))
+    qb = torch.randn((total, H, 576), device=DEV).bfloat16()
+    o, lse = tc.call(d, qb, cu, total, max(qs), pool, n_pages, table, i32(lens))
+    qn = qb.clone()
+    bad = torch.zeros((total, H), dtype=torch.bool, device=DEV)
+    for u, h in ((0, 0), (total - 1, H - 1), (qs[0] - 1, H // 2)):
+        qn[u, h, 7 + h] = NAN
+        bad[u, h] = True
+    o2, lse2 = tc.call(d, qn, cu, total, max(qs), pool, n_pages, table, i32(lens))
+    assert status() == 0
+    assert o2[bad].isnan().all() and lse2[bad].isnan().all()
+    assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
