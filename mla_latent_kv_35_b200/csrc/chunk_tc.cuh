@@ -72,11 +72,11 @@ __device__ __forceinline__ int block_exclusive(int x, int* warp_sums, int* total
   return before + inc - x;
 }
 
-// Whether cu_q breaks its rules at sequence b: ascending within [0, total_q],
-// no chunk longer than max_q.
+// Whether cu_q breaks its rules at sequence b: ascending from 0 to at most
+// total_q, no chunk longer than max_q.
 __device__ __forceinline__ bool chunk_bad(const int32_t* cu_q, int b, int total_q, int max_q) {
   const int a = cu_q[b], z = cu_q[b + 1];
-  return a < 0 || z < a || z > total_q || z - a > max_q;
+  return a < 0 || (b == 0 && a != 0) || z < a || z > total_q || z - a > max_q;
 }
 
 // Virtual sequences of the batch, sequence by sequence, and the prefix sums

@@ -137,3 +137,20 @@ def test_a_nan_query_gives_nan_however_it_is_split(H, qs, lens):
     assert status() == 0
     assert o2[bad].isnan().all() and lse2[bad].isnan().all()
     assert torch.equal(o2[~bad], o[~bad]) and torch.equal(lse2[~bad], lse[~bad])
+
+
+@gpu
+def test_chunks_that_do_not_begin_at_the_first_token():
+    """cu_q ascends from 0: a cu_q that begins later breaks its rules, and nothing is written."""
+    lens = [200, 300, 90]
+    d = dims("bf16", H=16)
+    pool, table, n_pages, _ = paged(np.random.default_rng(3), lens, 576, torch.bfloat16)
+    qb = torch.randn((9, 16, 576), device=DEV).bfloat16()
+    o, lse = tc.call(d, qb, i32([1, 2, 4, 5]), 9, 4, pool, n_pages, table, i32(lens))
+    assert status() == 5
+    assert (o == 5).all() and (lse == 5).all()
+    w = torch.full((3, 300), 9.0, device=DEV)
+    tw.call(d, qb, torch.full((9, 16), 8.0, device=DEV), i32([1, 2, 4, 5]), 9, 4, pool, n_pages, table, i32(lens),
+            None, 1.0, w)
+    assert status() == 5
+    assert (w == 9).all()
