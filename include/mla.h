@@ -507,7 +507,8 @@ mla_status mla_norm_rope(const mla_dims* dims, const void* y, int y_stride_tok, 
  * workspace: device, >= mla_cache_evict_workspace_size bytes, 256-byte
  * aligned, contents ignored.  A length outside [0, min(stride,
  * max_pages*page_size)] leaves that sequence as it was and raises
- * MLA_ERR_BOUNDS; so does a page id outside the pool, for the rows it holds. */
+ * MLA_ERR_BOUNDS.  So does a page id outside the pool: a pair with either slot
+ * on it is not moved, the vacated slot keeping row, weight and position. */
 size_t mla_cache_evict_workspace_size(const mla_dims* dims, int B, int stride);
 mla_status mla_cache_evict(const mla_dims* dims, void* pool, int n_pages, int fp8_rows,
                            const int32_t* page_table, int max_pages, const int32_t* seq_lens,

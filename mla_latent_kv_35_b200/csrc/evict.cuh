@@ -592,7 +592,8 @@ __global__ void __launch_bounds__(256) evict_move_kernel(
       raise_flag(kFlagBounds);
       row_to = -1;
     }
-    if (lane < count) {
+    // weight and position go with the row, or stay with it
+    if (lane < count && row_to >= 0) {
       const long long d = lb * stride;
       new_weights[d + to] = weights[d + from];
       if (new_pos != nullptr) new_pos[d + to] = slot_pos != nullptr ? slot_pos[d + from] : from;

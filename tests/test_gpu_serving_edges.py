@@ -154,3 +154,39 @@ def test_chunks_that_do_not_begin_at_the_first_token():
             None, 1.0, w)
     assert status() == 5
     assert (w == 9).all()
+
+
+@gpu
+@pytest.mark.parametrize("alias", [False, True])
+@pytest.mark.parametrize("bad_page", [0, 1])
+@pytest.mark.parametrize("drop", [10, 3])
+def test_eviction_around_a_bad_page_keeps_rows_and_books_together(alias, bad_page, drop):
+    """A pair whose source or destination lies on a page outside the pool is not moved at all: the
+    vacated slot keeps its row, its weight and its position."""
+    d = dims("bf16", dc=8, dr=0, page=16)
+    pool = torch.arange(5 * 16, device=DEV).bfloat16().view(5, 16, 1).repeat(1, 1, 8).contiguous()
+    before = pool.clone()
+    table = [[0, 1], [2, 3]]
+    table[0][bad_page] = 9 if bad_page else -1
+    W = torch.arange(48, device=DEV).float().repeat(2, 1)
+    P = (torch.arange(48, device=DEV, dtype=torch.int32) * 2).repeat(2, 1)
+    w, p, lens = W.clone(), P.clone(), i32([20, 20])
+    nw = w if alias else torch.full((2, 48), 77.0, device=DEV)
+    np_ = p if alias else torch.full((2, 48), 66, dtype=torch.int32, device=DEV)
+    nl = lens if alias else i32([0, 0])
+    ws = torch.empty(B.mla_cache_evict_workspace_size(d, 2, 48), dtype=torch.uint8, device=DEV)
+    B.mla_cache_evict(d, pool, 5, False, i32(table), 2, lens, 2, w, p, 48, i32([20 - drop] * 2), 0, 0, nw, np_, nl,
+                      ws)
+    assert status() == 5
+    new = 20 - drop
+    assert nl.tolist() == [new, new]
+    for b in range(2):
+        src = list(range(new))                         # the lightest, slots 0 .. drop - 1, leave
+        for k in range(drop):
+            if b == 1 or (table[0][0] == 0 and (new + k < 16 or table[0][1] == 1)):
+                src[k] = new + k
+        assert nw[b, :new].tolist() == W[b, src].tolist()
+        assert np_[b, :new].tolist() == P[b, src].tolist()
+        for t in range(new):
+            if table[b][t // 16] in range(5):
+                assert torch.equal(pool[table[b][t // 16], t % 16], before[table[b][src[t] // 16], src[t] % 16])
