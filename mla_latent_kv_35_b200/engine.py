@@ -285,21 +285,31 @@ class MLADecodeLayer:
         the least gathered weight leave, the first n_sink and the last
         n_recent positions excepted, and the survivors behind the new end move
         into their slots.  Updates pool, seq_lens, weights and slot_pos (int32
-        [B, tokens], the position of every slot's token; None while slots
-        follow positions) in place.  Any layer and cache kind.
+        [B, tokens], the position of every slot's token) in place and returns
+        slot_pos.  Any layer and cache kind.
 
-        New tokens then go to the slots from seq_lens on (places of step() and
-        extend()) at their own positions.  No page may belong to two sequences.
-        slot: an independent second workspace."""
+        slot_pos None: slots follow positions, as until the first eviction; the
+        positions that then hold are returned in a new tensor, its entries
+        from seq_lens on undefined.  The next eviction needs it, with the
+        positions of the tokens appended since written behind (by slots, sinks
+        and recent tokens would be others).
+
+        New tokens then go to the slots from seq_lens on (places of step()
+        and extend()) at their own positions.  No page may
+        belong to two sequences.  slot: an independent second workspace."""
         d = self.dims
         B, width = weights.shape
         key = ("evict", B, width, slot)
         if key not in self._bufs:
             self._bufs[key] = torch.empty((_b.mla_cache_evict_workspace_size(d, B, width),),
                                           dtype=torch.uint8, device=self.device)
+        new_pos = slot_pos
+        if new_pos is None:
+            new_pos = torch.empty((B, width), dtype=torch.int32, device=self.device)
         _b.mla_cache_evict(d, self.pool, self.n_pages, self.cache_kind == "fp8", self.page_table,
                            self.max_pages, self.seq_lens, B, weights, slot_pos, width, budget,
-                           n_sink, n_recent, weights, slot_pos, self.seq_lens, self._bufs[key])
+                           n_sink, n_recent, weights, new_pos, self.seq_lens, self._bufs[key])
+        return new_pos
 
     # ------------------------------------------------------------------
     # chunked prefill (non-absorbed)

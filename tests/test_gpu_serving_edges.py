@@ -190,3 +190,64 @@ def test_eviction_around_a_bad_page_keeps_rows_and_books_together(alias, bad_pag
         for t in range(new):
             if table[b][t // 16] in range(5):
                 assert torch.equal(pool[table[b][t // 16], t % 16], before[table[b][src[t] // 16], src[t] % 16])
+
+
+@gpu
+@pytest.mark.parametrize("captured", [False, True])
+def test_evictions_in_a_row_from_slots_in_order(captured):
+    """The first eviction knows positions by their slots and returns them for the next one, whose sinks
+    and recent tokens are then those of the sequence, not of the slots."""
+    layer, W, rng = make(norms=False, n_seqs=2, width=256)
+    lens = [200, 70]
+    layer.pool.normal_()
+    layer.seq_lens.copy_(i32(lens))
+    w = torch.rand((2, 256), device=DEV)
+    w[0, :4] = 0                                       # sinks and recent tokens are the lightest
+    w[0, 190:200] = 0
+    w[1, 60:70] = 0
+    W0, pos = w.cpu().numpy().copy(), [list(range(L)) for L in lens]
+    cuts = ([120, 50], [40, 20], [30, 19])
+
+    def loop():
+        slot_pos, kept = None, []
+        for cut in cuts:
+            slot_pos = layer.evict(w, budgets[str(cut)], 4, 10, slot_pos)
+            kept.append((slot_pos.clone(), w.clone(), layer.seq_lens.clone()))
+        return kept
+    budgets = {str(cut): i32(cut) for cut in cuts}
+    if captured:
+        state = [t.clone() for t in (layer.pool, layer.seq_lens, w)]
+        loop()                                         # allocates
+        side = torch.cuda.Stream()
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=side):
+            kept = loop()
+        for t, s in zip((layer.pool, layer.seq_lens, w), state):
+            t.copy_(s)
+        g.replay()
+    else:
+        kept = loop()
+    assert status() == 0
+    held = [W0[b, :L] for b, L in enumerate(lens)]
+    for cut, (sp, ww, ll) in zip(cuts, kept):
+        for b in range(2):
+            pairs, new = oracle.evict(held[b], pos[b], cut[b], 4, 10)
+            keep = list(range(new))
+            for to, frm in pairs:
+                keep[to] = frm
+            held[b], pos[b] = held[b][keep], [pos[b][k] for k in keep]
+            assert ll[b].item() == new
+            np.testing.assert_array_equal(sp[b, :new].cpu().numpy(), pos[b])
+            np.testing.assert_array_equal(ww[b, :new].cpu().numpy(), held[b])
+            assert set(range(4)) | set(range(lens[b] - 10, lens[b])) <= set(pos[b])
+
+
+@gpu
+def test_eviction_updates_the_positions_it_is_given():
+    layer, W, rng = make(norms=False, n_seqs=1, width=128)
+    layer.pool.normal_()
+    layer.seq_lens.fill_(100)
+    sp = torch.arange(128, dtype=torch.int32, device=DEV)[None].contiguous()
+    out = layer.evict(torch.rand((1, 128), device=DEV), i32([60]), 2, 5, sp)
+    assert out is sp and status() == 0 and len(set(sp[0, :60].tolist())) == 60
