@@ -294,8 +294,8 @@ class MLADecodeLayer:
         positions of the tokens appended since written behind (by slots, sinks
         and recent tokens would be others).
 
-        New tokens then go to the slots from seq_lens on (places of step()
-        and extend()) at their own positions.  No page may
+        New tokens then go to the slots from seq_lens on (places of step(),
+        extend() and prefill_chunk()) at their own positions.  No page may
         belong to two sequences.  slot: an independent second workspace."""
         d = self.dims
         B, width = weights.shape
@@ -334,11 +334,14 @@ class MLADecodeLayer:
             )
         return self._bufs[key]
 
-    def prefill_chunk(self, h, pos, batch_idx, b: int, T: int, L: int, slot: int = 0):
+    def prefill_chunk(self, h, pos, batch_idx, b: int, T: int, L: int, slot: int = 0,
+                      places=None):
         """Prefill T new tokens of sequence b, at positions L - T .. L - 1.
 
         h [T, d_model] device; pos int32 [T] = L - T .. L - 1 and batch_idx
-        int32 [T] = b, both on the device.  The chunk takes the non-absorbed
+        int32 [T] = b, both on the device.  places: int32 [T] device = L - T ..
+        L - 1, the slots of the new tokens where they differ from pos (after
+        evict), L then being the cached tokens.  The chunk takes the non-absorbed
         form: the new tokens' latents and RoPE keys go into the cache, then
         every head's keys and values of all L tokens are rebuilt once
         (W_UK c, W_UV c) and the T queries attend causally over them.
@@ -363,13 +366,14 @@ class MLADecodeLayer:
         bf = self.prefill_buffers(T, L, slot)
         y = bf["y"]
         _b.mla_project(d, h, self.W_A0, y, T, d.d_model, Y)
+        places = pos if places is None else places
         if self.normed:
-            self._norm_rope_append(y, None, batch_idx, pos, pos, T)
+            self._norm_rope_append(y, None, batch_idx, pos, places, T)
         else:
             _b.mla_rope(d, y[:, dn:], Y, dqk, H, y[:, dn:], Y, dqk, pos, T)
             kr = y[:, off_c + dc:]
             _b.mla_rope(d, kr, Y, 0, 1, kr, Y, 0, pos, T)
-            _b.mla_cache_append(d, y[:, off_c:], Y, kr, Y, batch_idx, pos, self.page_table,
+            _b.mla_cache_append(d, y[:, off_c:], Y, kr, Y, batch_idx, places, self.page_table,
                                 self.max_pages, self.pool, self.n_pages, T)
         _b.mla_prefill_rebuild_kv(d, self.pool, self.n_pages, self.page_table[b], L, self.W_UK,
                                   self.W_UV, bf["ctx"], bf["k_nope"], bf["v"])
@@ -410,10 +414,13 @@ class DecodePipeline:
     inputs are in (and the slot's previous output has left), and the output
     is copied back on a download stream while the next step computes.  Every
     step still moves its own inputs in and its own output out.
+
+    placed: the steps take places beside positions, as they have to once
+    tokens were evicted.
     """
 
     def __init__(self, layer: MLADecodeLayer, B: int, S_q: int, num_workers: int = 0,
-                 fused: bool = True):
+                 fused: bool = True, placed: bool = False):
         d = layer.dims
         dev = layer.device
         T = B * S_q
@@ -425,19 +432,24 @@ class DecodePipeline:
             h = torch.zeros((T, d.d_model), dtype=d.torch_dtype, device=dev)
             bi = torch.zeros((T,), dtype=torch.int32, device=dev)
             pos = torch.zeros((T,), dtype=torch.int32, device=dev)
-            graph, bf, kernels = layer.capture(h, bi, pos, B, S_q, num_workers, fused, slot=s)
-            self.slots.append(dict(h=h, bi=bi, pos=pos, graph=graph, out=bf["out"],
+            places = torch.zeros((T,), dtype=torch.int32, device=dev) if placed else None
+            graph, bf, kernels = layer.capture(h, bi, pos, B, S_q, num_workers, fused, slot=s,
+                                               places=places)
+            self.slots.append(dict(h=h, bi=bi, pos=pos, places=places, graph=graph, out=bf["out"],
                                    inputs_in=torch.cuda.Event(), done=torch.cuda.Event(),
                                    out_read=torch.cuda.Event()))
         self.kernels_per_step = kernels
         self.i = 0
 
-    def submit(self, h_host, bi_host, pos_host, out_host):
+    def submit(self, h_host, bi_host, pos_host, out_host, places_host=None):
         """Enqueue one step: h_host [T, d_model], bi_host/pos_host int32 [T]
         and out_host fp32 [T, d_model] are pinned host tensors; out_host
         holds the step's output once the step's `out_read` event has
-        completed (after wait(), at the latest)."""
+        completed (after wait(), at the latest).  places_host int32 [T],
+        pinned: with placed=True, and only then."""
         sl = self.slots[self.i % 2]
+        if (places_host is None) != (sl["places"] is None):
+            raise ValueError("places go with a pipeline made with placed=True")
         self.i += 1
         compute = torch.cuda.current_stream(self.layer.device)
         # the slot's inputs are free once its previous step has run
@@ -446,6 +458,8 @@ class DecodePipeline:
             sl["h"].copy_(h_host, non_blocking=True)
             sl["bi"].copy_(bi_host, non_blocking=True)
             sl["pos"].copy_(pos_host, non_blocking=True)
+            if places_host is not None:
+                sl["places"].copy_(places_host, non_blocking=True)
             sl["inputs_in"].record(self.up)
         compute.wait_event(sl["inputs_in"])
         compute.wait_event(sl["out_read"])
@@ -496,15 +510,17 @@ class PrefillPipeline:
                 h=torch.empty((T, d.d_model), dtype=d.torch_dtype, device=dev),
                 bi=torch.empty((T,), dtype=torch.int32, device=dev),
                 pos=torch.empty((T,), dtype=torch.int32, device=dev),
+                places=torch.empty((T,), dtype=torch.int32, device=dev),
                 inputs_in=torch.cuda.Event(), done=torch.cuda.Event(),
                 out_read=torch.cuda.Event()))
         self.i = 0
 
-    def submit(self, h_host, bi_host, pos_host, out_host):
+    def submit(self, h_host, bi_host, pos_host, out_host, places_host=None):
         """Enqueue one chunk: h_host [T, d_model] (layer dtype), bi_host and
         pos_host int32 [T] and out_host [T, d_model] (layer dtype) are pinned
         host tensors; out_host holds the chunk's output once its `out_read`
-        event (returned) has completed."""
+        event (returned) has completed.  places_host int32 [T], pinned: the
+        places of prefill_chunk, or None."""
         s = self.i % 2
         sl = self.slots[s]
         self.i += 1
@@ -514,11 +530,13 @@ class PrefillPipeline:
             sl["h"].copy_(h_host, non_blocking=True)
             sl["bi"].copy_(bi_host, non_blocking=True)
             sl["pos"].copy_(pos_host, non_blocking=True)
+            if places_host is not None:
+                sl["places"].copy_(places_host, non_blocking=True)
             sl["inputs_in"].record(self.up)
         compute.wait_event(sl["inputs_in"])
         compute.wait_event(sl["out_read"])
         bf = self.layer.prefill_chunk(sl["h"], sl["pos"], sl["bi"], self.b, self.T, self.L,
-                                      slot=s)
+                                      slot=s, places=None if places_host is None else sl["places"])
         sl["done"].record(compute)
         self.down.wait_event(sl["done"])
         with torch.cuda.stream(self.down):

@@ -251,3 +251,87 @@ def test_eviction_updates_the_positions_it_is_given():
     sp = torch.arange(128, dtype=torch.int32, device=DEV)[None].contiguous()
     out = layer.evict(torch.rand((1, 128), device=DEV), i32([60]), 2, 5, sp)
     assert out is sp and status() == 0 and len(set(sp[0, :60].tolist())) == 60
+
+
+def _evicted(n_seqs, seed, norms=True):
+    """A layer whose caches were cut, its reference, and what a loop then knows: cached tokens and next
+    positions of every sequence."""
+    layer, W, rng = make(norms=norms, n_seqs=n_seqs, seed=seed)
+    d, ctx, cut = layer.dims, [150, 70, 64][:n_seqs], [90, 70, 31][:n_seqs]
+    h_ctx = [q(rng.standard_normal((k, d.d_model)), "bf16") for k in ctx]
+    layer.prefill_from_hidden(h_ctx)
+    layer.seq_lens.copy_(i32(ctx))
+    ref = Reference(d, W, n_seqs)
+    w = torch.rand((n_seqs, 512), device=DEV)
+    held = w.cpu().numpy()
+    sp = layer.evict(w, i32(cut), 2, 5)
+    for b in range(n_seqs):
+        rows = ref.new_rows(h_ctx[b], np.arange(ctx[b]))[1]
+        pairs, new = oracle.evict(held[b, :ctx[b]], list(range(ctx[b])), cut[b], 2, 5)
+        assert new == cut[b]
+        keep = list(range(new))
+        for to, frm in pairs:
+            keep[to] = frm
+        ref.rows[b] = rows[keep]
+    assert status() == 0
+    return layer, ref, rng, cut, ctx, sp
+
+
+TOL = dict(max_abs=6e-2, mean_abs=6e-3, rel_l2=2e-2)       # as for the loop of test_gpu_serving
+
+
+@gpu
+@pytest.mark.parametrize("norms", [True, False])
+def test_prefill_chunk_behind_an_eviction(norms):
+    layer, ref, rng, cut, ctx, _ = _evicted(1, 21, norms)
+    T = 100
+    h, bi, pos, places = tokens(rng, layer, [T], ctx, cut)
+    before = layer.pool.clone()
+    bf = layer.prefill_chunk(to_dev(h, "bf16"), i32(pos), i32(bi), 0, T, cut[0] + T, places=i32(places))
+    assert status() == 0
+    out, _, lse, _ = ref.extend(h, [0, T], pos)
+    check(to_np(bf["out"]), out, "bf16", "out", TOL)
+    check(to_np(bf["lse"]), lse, "bf16", "lse", dict(max_abs=6e-2, mean_abs=6e-3))
+    table = layer.page_table[0].cpu().numpy()
+    a, z = bits(before), bits(layer.pool)
+    changed = [s for s in range(512) if (a[table[s // 64], s % 64] != z[table[s // 64], s % 64]).any()]
+    assert changed == list(range(cut[0], cut[0] + T))
+
+
+@gpu
+def test_pipelines_behind_an_eviction():
+    n = 3
+    layer, ref, rng, cut, ctx, _ = _evicted(n, 22)
+    pipe = DecodePipeline(layer, n, 1, placed=True)
+    outs, want = [], []
+    pin = lambda x, t: torch.from_numpy(np.asarray(x)).to(t).pin_memory()  # noqa: E731
+    lens, nxt = list(cut), list(ctx)
+    start = layer.pool.clone()
+    steps = [tokens(rng, layer, [1] * n, [p + k for p in nxt], [L + k for L in lens]) for k in range(3)]
+    for k, (h, bi, pos, places) in enumerate(steps):
+        pipe.wait()
+        layer.seq_lens.copy_(i32([L + k + 1 for L in lens]))
+        out = torch.empty((n, 256)).pin_memory()
+        pipe.submit(pin(h, torch.bfloat16), pin(bi, torch.int32), pin(pos, torch.int32), out,
+                    pin(places, torch.int32))
+        outs.append(out)
+        want.append(ref.extend(h, np.arange(n + 1), pos)[0])
+    pipe.wait()
+    assert status() == 0
+    for got, w in zip(outs, want):
+        check(got.numpy(), w, "bf16", "out", TOL)
+    with pytest.raises(ValueError):
+        pipe.submit(None, None, None, None)
+    with pytest.raises(ValueError):
+        DecodePipeline(layer, n, 1).submit(None, None, None, None, torch.zeros(n, dtype=torch.int32))
+    # the same tokens as one chunk of the first sequence, through the prefill pipeline
+    layer.pool.copy_(start)
+    h = np.concatenate([s[0][:1] for s in steps])
+    pos, places, zero = np.arange(3) + ctx[0], np.arange(3) + cut[0], np.zeros(3)
+    pipe = PrefillPipeline(layer, 0, 3, cut[0] + 3)
+    out = torch.empty((3, 256), dtype=torch.bfloat16).pin_memory()
+    pipe.submit(pin(h, torch.bfloat16), pin(zero, torch.int32), pin(pos, torch.int32), out,
+                pin(places, torch.int32))
+    pipe.wait()
+    assert status() == 0
+    check(out.float().numpy(), np.stack([w[0] for w in want]), "bf16", "out", TOL)
