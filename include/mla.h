@@ -390,8 +390,8 @@ mla_status mla_prefill_attention(const mla_dims* dims, const void* q, int q_stri
  *   t <= L - T_b + j,   o_lat[u, i, :] = sum_t p_t pool_row(b, t)[0 : d_latent]
  *   lse[u, i] = ln sum_t exp(s_t)
  * qbuf: device bf16 [total_q, H, d_latent + d_rope]; cu_q: device int32
- * [B + 1], ascending from 0 to at most total_q, no chunk longer than max_q
- * (T_b = 0 is allowed); pool, page_table, seq_lens as for mla_decode; o_lat:
+ * [B + 1], ascending from 0 to at most total_q, no chunk longer than max_q <=
+ * total_q (T_b = 0 is allowed); pool, page_table, seq_lens as for mla_decode; o_lat:
  * device bf16 [total_q, H, d_latent] (the input of mla_out_proj_bf16); lse:
  * device fp32 [total_q, H].  Rows from cu_q[B] on are left as they were.
  * Accumulation, softmax and merges are fp32; p is rounded to bf16 for the

@@ -244,7 +244,8 @@ class MLADecodeLayer:
         seq_lens[b] cached tokens.
 
         cu_q int32 [B+1] device, batch_idx and pos int32 [T] device, max_q >=
-        the longest chunk; places as for step().  Decode tokens, speculative
+        the longest chunk (of every step a program makes, say; it may exceed
+        T); places as for step().  Decode tokens, speculative
         tokens and prompt tails go through one call.  Rows of h from cu_q[B]
         on are padding (a captured graph replays with the chunks that cu_q then
         holds): what out and o_lat hold for them is undefined, and their
@@ -262,7 +263,7 @@ class MLADecodeLayer:
         bf = self.extend_buffers(B, T, max_q, slot)
         _b.mla_project(d, h, self.W_A0, bf["y"], T, d.d_model, self.Y)
         self._pre_attention(bf, batch_idx, pos, places, T, fused)
-        _b.mla_chunk_attention(d, bf["qbuf"], cu_q, T, max_q, self.pool, self.n_pages,
+        _b.mla_chunk_attention(d, bf["qbuf"], cu_q, T, min(max_q, T), self.pool, self.n_pages,
                                self.page_table, self.max_pages, self.seq_lens, B, bf["ws"],
                                bf["o_lat"], bf["lse"])
         _b.mla_out_proj_bf16(d, bf["o_lat"], self.W_UV, self.W_O, bf["scratch"], bf["out"], T)
@@ -275,7 +276,7 @@ class MLADecodeLayer:
         step's own tokens start from nothing.  For a step, cu_q is 0, S_q,
         2 S_q, .. and T = B*S_q."""
         self._absorbed_only("gather_weights")
-        _b.mla_attn_weights(self.dims, bf["qbuf"], bf["lse"], cu_q, T, max_q, self.pool,
+        _b.mla_attn_weights(self.dims, bf["qbuf"], bf["lse"], cu_q, T, min(max_q, T), self.pool,
                             self.n_pages, self.page_table, self.max_pages, self.seq_lens,
                             self.page_table.shape[0], weights, keep, weights, weights.shape[1])
 

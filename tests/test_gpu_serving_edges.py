@@ -335,3 +335,24 @@ def test_pipelines_behind_an_eviction():
     pipe.wait()
     assert status() == 0
     check(out.float().numpy(), np.stack([w[0] for w in want]), "bf16", "out", TOL)
+
+
+@gpu
+def test_a_longest_chunk_above_the_tokens_there_are():
+    """max_q bounds the chunks of every step a program makes; a step may have fewer tokens than that."""
+    layer, W, rng = make(norms=False, n_seqs=2)
+    ctx = [30, 100]
+    layer.prefill_from_hidden([q(rng.standard_normal((k, 256)), "bf16") for k in ctx])
+    h, bi, pos, _ = tokens(rng, layer, [1, 2], ctx, ctx)
+    layer.seq_lens.copy_(i32([31, 102]))
+    args = (to_dev(h, "bf16"), i32(bi), i32(pos), i32([0, 1, 3]), 3)
+    got = []
+    for max_q in (2, 64):
+        bf = layer.extend(*args, max_q)
+        w = torch.zeros((2, 128), device=DEV)
+        layer.gather_weights(bf, args[3], 3, max_q, w)
+        got.append([bf["out"].clone(), w])
+    assert status() == 0
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+    layer.extend(args[0][:0], args[1], args[2], args[3] * 0, 0, 64)
+    assert status() == 0
