@@ -151,7 +151,6 @@ def lib():
             f = getattr(h, name)
             f.argtypes = args
             f.restype = res
-        _bind(h)
         _lib = h
     return _lib
 
@@ -162,8 +161,8 @@ def _bind(h):
     try:
         from . import _pycall as m
     except ImportError as e:
-        raise ImportError("the Python calls are missing: build them with "
-                          "`python -m mla_latent_kv_35_b200.build`") from e
+        raise ImportError("the Python calls are missing, or were built for another Python or "
+                          "torch: build them with `python -m mla_latent_kv_35_b200.build`") from e
     m.bind(*(ctypes.cast(getattr(h, f), _P).value for f in (
         "mla_chunk_attention", "mla_attn_weights", "mla_out_proj_bf16", "mla_norm_rope",
         "mla_cache_evict")))
@@ -204,8 +203,8 @@ def _native():
     tensors on the current device, contiguous, of the right type and large enough, or ValueError.
     (y, q and ckr of mla_norm_rope may be views of rows at the stride they come with, contiguous
     within a row.)"""
-    if _lib is None:
-        lib()
+    if _pycall is None:
+        _bind(lib())
     return _pycall
 
 

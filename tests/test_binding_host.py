@@ -143,3 +143,49 @@ def test_tensor_core_softmaxes_refuse_a_negative_scale():
         assert B.mla_decode_config(d, 1)[0] == (B.DECODE_KERNEL_SIMT if refused else B.DECODE_KERNEL_TC)
     assert lib.mla_chunk_attention(ctypes.byref(B.MLADims(16, 128, 512, 64, 128, 64, 64, -0.1, 1e4, "bf16").c()),
                                    x, x, 8, 4, x, 4, x, 2, x, 2, x, 1 << 40, x, x, 0) == 2
+
+
+def test_the_library_loads_without_the_native_calls(monkeypatch):
+    """Only the calls that go through the extension need it; they say what is missing."""
+    from mla_latent_kv_35_b200 import build
+    build.build()
+    monkeypatch.setitem(sys.modules, "mla_latent_kv_35_b200._pycall", None)      # its import fails
+    import mla_latent_kv_35_b200 as pkg
+    monkeypatch.delattr(pkg, "_pycall", raising=False)
+    monkeypatch.setattr(B, "_lib", None)
+    monkeypatch.setattr(B, "_pycall", None)
+    assert B.mla_status_string(0) == "ok"
+    assert B.mla_decode_workspace_size(dims(), 2, 1) > 0
+    assert B.mla_cache_evict_workspace_size(dims(), 2, 100) > 0
+    monkeypatch.setattr(B, "_where", lambda: (-1, 0))
+    with pytest.raises(ImportError, match="mla_latent_kv_35_b200.build"):
+        B.mla_out_proj_bf16(dims(), None, None, None, None, None, 0)
+
+
+def test_native_calls_of_another_python_or_torch_are_built_again(monkeypatch, tmp_path):
+    import shutil
+    from mla_latent_kv_35_b200 import build
+    build.build()
+    assert build.calls_up_to_date()
+    lib = {t: (tmp_path / n) for t, n in (("CALLS", "_pycall.so"), ("CALLS_STAMP", "stamp"))}
+    for t, p in lib.items():
+        shutil.copy2(getattr(build, t), p)
+        monkeypatch.setattr(build, t, str(p))
+    built = []
+    monkeypatch.setattr(build, "_compile", lambda cmd, target, verbose: built.append(target))
+    build.build()
+    assert built == []
+    for name in ("torch", "python"):
+        with monkeypatch.context() as m:
+            if name == "torch":
+                m.setattr(torch, "__version__", "0.0.0")
+            else:
+                m.setattr(sys, "version", "0.0.0")
+            assert not build.calls_up_to_date()
+            built.clear()
+            build.build()
+            assert built == [build.CALLS] and build.calls_up_to_date()
+        assert not build.calls_up_to_date()            # the stamp is the other one's now
+        build.build()
+    lib["CALLS_STAMP"].unlink()
+    assert not build.calls_up_to_date()
