@@ -209,12 +209,24 @@ class MLADecodeLayer:
         if self.dims.dtype != "bf16" or self.cache_kind != "bf16":
             raise ValueError(f"{what} needs a bf16 layer and a bf16 cache")
 
+    def _chunk_workspace(self, B: int, rows: int, slot: int):
+        """The chunk attention's workspace, one for all sets of up to 8192 rows
+        of a slot: nearly all of it, partial results of 39 MB, does not depend
+        on the rows (the rest is at most 24 bytes per 128 query rows)."""
+        rows = max(rows, 8192)
+        key = ("extend_ws", B, rows, slot)
+        if key not in self._bufs:
+            size = _b.mla_chunk_attention_workspace_size(self.dims, B, rows, rows)
+            self._bufs[key] = torch.empty((size,), dtype=torch.uint8, device=self.device)
+        return self._bufs[key]
+
     def extend_buffers(self, B: int, T: int, max_q: int, slot: int = 0):
         """Device buffers of one extend() of B sequences and T tokens, valid
         until the next extend() of this slot (slot: an independent second set,
         for calls or captured graphs that overlap).  They are views of sets
         whose rows are powers of two: the number of tokens differs from step
-        to step, and the memory is at most that of four sets of the longest."""
+        to step, and the memory stays within five times what the longest needs
+        by itself.  (None of it depends on max_q.)"""
         rows = 1 << (T - 1).bit_length() if T > 0 else 1
         key = ("extend", B, rows, slot)
         if key not in self._bufs:
@@ -229,8 +241,7 @@ class MLADecodeLayer:
                 o_lat=torch.empty((rows, H, d.d_latent), dtype=dt, device=dev),
                 lse=torch.empty((rows, H), dtype=torch.float32, device=dev),
                 out=torch.empty((rows, d.d_model), dtype=torch.float32, device=dev),
-                ws=torch.empty((_b.mla_chunk_attention_workspace_size(d, B, rows, rows),),
-                               dtype=torch.uint8, device=dev),
+                ws=self._chunk_workspace(B, rows, slot),
                 scratch=torch.empty((scratch,), dtype=torch.uint8, device=dev))
         full = self._bufs[key]
         if rows == T:

@@ -189,3 +189,34 @@ def test_native_calls_of_another_python_or_torch_are_built_again(monkeypatch, tm
         build.build()
     lib["CALLS_STAMP"].unlink()
     assert not build.calls_up_to_date()
+
+
+@pytest.mark.parametrize("H,dm,most", [(1, 64, 1100), (16, 5120, 1100), (128, 5120, 140)])
+def test_memory_of_the_buffers_of_many_step_lengths(H, dm, most):
+    """Steps of every length up to `most` hold at most five times what the longest one needs by itself."""
+    import numpy as np
+    from mla_latent_kv_35_b200 import build
+    from mla_latent_kv_35_b200.engine import MLADecodeLayer
+    build.build()
+    d = B.MLADims(H, 128, 512, 64, 128, dm, 64, 0.1, 10000.0, "bf16")
+    none = np.zeros((0, 1), np.float32)
+    layer = MLADecodeLayer(d, {k: none for k in ("W_Q", "W_DKV", "W_KR", "W_UK", "W_UV", "W_O")}, "cpu")
+
+    def held():
+        s = {}
+        for v in layer._bufs.values():
+            for t in v.values() if isinstance(v, dict) else [v]:
+                s[t.untyped_storage().data_ptr()] = t.untyped_storage().nbytes()
+        return sum(s.values())
+    for nB in (1, 64):
+        T = 1
+        while T <= most:
+            bf = layer.extend_buffers(nB, T, T)
+            assert bf["ws"].numel() >= B.mla_chunk_attention_workspace_size(d, nB, T, T)
+            assert bf["scratch"].numel() >= B.mla_out_proj_bf16_scratch_size(d, T)
+            row = 2 * (layer.Y + H * (576 + 512)) + 4 * (H + dm)
+            alone = (T * row + B.mla_chunk_attention_workspace_size(d, nB, T, T) +
+                     B.mla_out_proj_bf16_scratch_size(d, T))
+            assert held() <= 5 * alone, (nB, T, held() / alone)
+            T += max(1, T // 5)
+        layer._bufs.clear()
