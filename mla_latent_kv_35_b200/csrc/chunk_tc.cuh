@@ -36,7 +36,8 @@
 //   * o is stored in bf16: it is the W_UV product's input, and P is bf16.
 //
 // Bound: the tensor pipe and the loads that feed it.  128 rows meet each
-// 576-number row of the cache, 242 operations per byte read through L2.
+// 576-number row of the cache, which comes through L2 as a key (1152 bytes) and
+// again as a value (1024): 128 operations per byte.
 #pragma once
 
 #include "decode_tc.cuh"

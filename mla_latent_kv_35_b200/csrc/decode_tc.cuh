@@ -66,7 +66,8 @@
 //     combine kernel merges them.
 //
 // Shared memory: Q 72 KB + QK ring 96 KB + PV ring 48 KB + P exchange 8 KB
-// (also the row sums of the epilogue), 1.2 KB of barriers and row maxima.
+// (the epilogue turns O around in it), 1.2 KB of barriers and row maxima (the
+// epilogue's row sums meet in their place).
 //
 // Partial and missing pages.  QK boxes always load a whole page; slots past
 // the sequence hold whatever the pool holds there and are masked by index in

@@ -67,20 +67,14 @@ constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxStages = 9;
 // Pages that the start of a sequence counts for in the split of resident
 // queries: its queries are loaded and one more partial tile is worked.
-#ifndef MLA_WEIGHTS_OPEN
-#define MLA_WEIGHTS_OPEN 3
-#endif
-constexpr int kOpenPages = MLA_WEIGHTS_OPEN;
-#ifndef MLA_WEIGHTS_CHUNKS
-#define MLA_WEIGHTS_CHUNKS 3
-#endif
+constexpr int kOpenPages = 3;
 template <bool kQStat, int kN>
 struct Shape {
   static constexpr int kStat = kQStat ? 9 * (kN / 2) * 128 : kTileBytes;       // stationary bytes
   // A stage: kCps 64-column chunks of 128 tokens, or one of kN / 2 query rows.
-  static constexpr int kCps = !kQStat ? 1 : kN == 128 ? MLA_WEIGHTS_CHUNKS : 1;
+  static constexpr int kCps = kQStat && kN == 128 ? 3 : 1;
   static constexpr int kStage = kQStat ? kCps * 128 * 128 : (kN / 2) * 128;
-  static constexpr int kSteps = (9 + kCps - 1) / kCps;                          // per tile or row block
+  static constexpr int kSteps = 9 / kCps;                                       // per tile or row block
   static constexpr int kRing = kStat > 100 * 1024 ? 64 * 1024 : 144 * 1024;
   static constexpr int kStages = kRing / kStage;
   static constexpr int kBufs = (int)kTmemCols / kN;                             // S buffers
@@ -442,12 +436,10 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(wtc::kThreads, 1)
           if (!fresh && !done) {
             tc_fence_after();
 #pragma unroll
-            for (int cc = 0; cc < S::kCps; ++cc)
-              if (k * S::kCps + cc < 9) issue(cc);
+            for (int cc = 0; cc < S::kCps; ++cc) issue(cc);
           } else {
             for (int cc = 0; cc < S::kCps && ok; ++cc) {
               const int c = k * S::kCps + cc;
-              if (c >= 9) break;               // past the 576 columns
               ok = !fresh || mbar_wait(smem_u32(&stat_full[c]), stats & 1, abort_p, 42, stats);
               if (!ok) break;
               tc_fence_after();
