@@ -43,9 +43,9 @@
 //
 // Bound: the plan by latency (loads, then three to six cluster barriers) and by
 // instruction issue (32 warps on one SM), the move by memory bandwidth.
-// Measured in a graph: one token of 16 x 4097 8.0 us, 64 sequences
-// of 129 to 32769 tokens to 30 % 52 us (plan 18.5), 4 x 131072 halved 76 us
-// (plan 21).
+// Measured in a graph: one token of 16 x 4097 8.2 us (8.8 with positions), 64
+// sequences of 129 to 32769 tokens to 30 % 53 us (plan 18.5), 4 x 131072 halved
+// 76 to 79 us (plan 21).
 #pragma once
 
 #include "common.cuh"
@@ -60,9 +60,10 @@ constexpr int kEvictBins = 2048;
 // thread: with 1024 threads the plan is bound by instruction issue), else 16.
 constexpr int kEvictFewKeys = 8, kEvictKeys = 16;
 // Up to so many tokens of a sequence leave one after the other, as when every
-// decode step adds a few to a full budget: 1.3 us each for 4097 tokens (one
-// token: 8.0 us with its move against 12.3 by the histograms, two 9.8, four
-// 12.2), 2.8 us for 131072 (12.6 against 23.3, four 21.5).
+// decode step adds a few to a full budget: 1.3 to 1.6 us each for 4097 tokens
+// (one token: 8.2 us with its move, 8.8 with positions, against 12.3 by the
+// histograms; four take 12.2 either way), 3 us for 131072 (one: 13.5, 15.4 with
+// positions, against 23.3; four 21.5 against 23.5).
 constexpr int kEvictPicks = 3;
 constexpr int kEvictGroups = 2048;                          // sequence groups of the move
 

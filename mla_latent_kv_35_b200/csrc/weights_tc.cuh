@@ -32,13 +32,14 @@
 // each weighing the row blocks it meets.  Every CTA finds its run itself (a
 // scan over the sequences), so there is no planning launch and no workspace.
 //
-// Measured: 64 ragged sequences of 129 to 65537 tokens (991 MB) 157 to 162 us
-// in a graph, 6.1 to 6.3 TB/s, boxes of three 64-column chunks (one: 203, two:
-// 190, three: 182 us with the cache flushed); 16 x 4096 tokens 18.5 us, the
-// start of a sequence counted as three pages in the split (none: 32.0, three:
-// 28.7 us with the launch).  4 x 32 queries over 8 K tokens 135 to 142 us: 693
-// clocks per 64-column stage against 512 of MMA, about 64 KB of shared memory
-// traffic each, and two tiles for most pairs against 1.73 on average.
+// Measured: 64 ragged sequences of 129 to 65537 tokens (991 MB) 157 to 166 us
+// in a graph, 6.0 to 6.3 TB/s, boxes of three 64-column chunks (one: 203, two:
+// 190, three: 182 us with the cache flushed); 16 x 4096 tokens 18.5 to 19 us,
+// the start of a sequence counted as three pages in the split (none: 32.0,
+// three: 28.7 us with the launch).  4 x 32 queries over 8 K tokens 126 us in a
+// graph: 693 clocks per 64-column stage against 512 of MMA, about 64 KB of
+// shared memory traffic each, and two tiles for most pairs against 1.73 on
+// average.
 //
 // Row sums: four chains per thread over 32 columns at a time, fp32.  Rows
 // whose lse is -inf (a query that saw nothing) or +inf give nothing; one whose
