@@ -118,8 +118,8 @@ struct Args {
   }
 
   // address of `rows` rows of `width` elements, `stride` apart: a contiguous
-  // tensor that holds them all, or a view whose first dimension are rows at
-  // that stride, each contiguous and wide enough
+  // tensor that holds them all, or a view whose last dimensions are contiguous
+  // rows, wide enough, and whose first ones lie at that stride
   void* rows(const char* what, PyObject* o, at::ScalarType type, long long rows, long long width,
              long long stride) {
     const at::Tensor* t = placed(what, o, type);
@@ -135,13 +135,14 @@ struct Args {
   }
   static bool holds_rows(const at::Tensor& t, long long rows, long long width, long long stride) {
     if (t.is_contiguous()) return t.numel() >= (rows - 1) * stride + width;
-    if (t.dim() < 2 || t.size(0) < rows || (rows > 1 && t.stride(0) != stride)) return false;
-    long long inner = 1;                    // numbers of a row's last dimensions
-    for (long long i = t.dim() - 1; i > 0; --i) {
-      if (t.size(i) != 1 && t.stride(i) != inner) return false;
-      inner *= t.size(i);
+    long long inner = 1, n = 1, i = t.dim() - 1;     // numbers of a row, and rows
+    for (; i >= 0 && (t.size(i) == 1 || t.stride(i) == inner); --i) inner *= t.size(i);
+    if (rows == 1) return inner >= width;
+    for (; i >= 0; --i) {
+      if (t.size(i) != 1 && t.stride(i) != n * stride) return false;
+      n *= t.size(i);
     }
-    return inner >= width;
+    return inner >= width && n >= rows;
   }
 
   // the C call's status; other Python threads run meanwhile

@@ -99,6 +99,12 @@ def test_rows_at_a_stride_lie_within_their_tensor(norm, name, stride, width):
     reaches_the_library(rows(3, width).view(3, -1, 1, width // 2), width)
     reaches_the_library(big[1:2, 5:], width, 1)                          # one row: any stride
     reaches_the_library(big[1:3, 5:], width, 1)
+    reaches_the_library(big.view(2, 4, -1)[..., 5:], width + 5, 8)       # tokens in two dimensions
+    reaches_the_library(big.view(2, 4, -1)[..., 5:].view(2, 4, 2, -1), width + 5, 8)
+    reaches_the_library(big.view(8, 1, -1)[..., 5:], width + 5, 8)
+    refused(big.view(2, 4, -1)[:, :3, 5:], width + 5, 6)                 # not at one stride
+    refused(big.view(2, 4, -1)[..., 5:], width + 5, 9)
+    refused(big.view(2, 4, -1).transpose(0, 1)[..., 5:], width + 5, 8)
     refused(big[:2], width + 5)                                          # fewer rows than tokens
     refused(big[:2, 5:], width + 5)
     refused(big.view(-1)[:2 * (width + 5) + width - 1], width + 5)
